@@ -1,5 +1,6 @@
 """ctypes binding over the C ABI in ``include/gemv.h``,
-``include/gemv_quant.h`` and ``include/gemv_softmax.h``.
+``include/gemv_quant.h``, ``include/gemv_softmax.h``,
+``include/gemv_tokens.h`` and ``include/gemv_attention.h``.
 
 Argument marshalling only: every step of the product runs in the HIP
 library.  PyTorch supplies device memory and the current stream; no torch
@@ -16,6 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgemv_amd.so")
 
 KIND = {"f32": 0, "f16": 1, "q8": 2, "q4": 3, "f16x32": 4, "f16_acc16": 5}
+DTYPE = {"float32": 0, "float16": 1, "bfloat16": 2}   # gemv_dtype
 STATUS = {0: "GEMV_OK", 1: "GEMV_E_INVAL", 2: "GEMV_E_UNSUPPORTED", 3: "GEMV_E_LAUNCH", 4: "GEMV_E_DEVICE"}
 
 _lock = threading.Lock()
@@ -39,6 +41,19 @@ class Plan(ctypes.Structure):
     rows_per_wave, stage_order, cap)."""
     _fields_ = [("variant", ctypes.c_int), ("waves", ctypes.c_int), ("units_in_flight", ctypes.c_int),
                 ("rows_per_wave", ctypes.c_int), ("stage_order", ctypes.c_int), ("cap", ctypes.c_int)]
+
+
+class KvCache(ctypes.Structure):
+    """gemv_kv_cache: the pages of a key-value cache and how they lie."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("stride_page", ctypes.c_int64), ("stride_slot", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class KvBatch(ctypes.Structure):
+    """gemv_kv_batch: the sequences of a call."""
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("width", ctypes.c_int),
+                ("lens", ctypes.c_void_p), ("batch", ctypes.c_int), ("max_len", ctypes.c_int)]
 
 
 def load():
@@ -77,6 +92,22 @@ def load():
         lib.gemv_check_plan_for.restype = i
         lib.gemv_launch_plan.argtypes = [i, p, p, p, p, i, i, ctypes.POINTER(Plan), p]
         lib.gemv_launch_plan.restype = i
+        i64, z = ctypes.c_int64, ctypes.c_size_t
+        lib.gemv_quantize_tokens_q8.argtypes = [p, i, i64, p, p, i, i, p]
+        lib.gemv_quantize_tokens_q8.restype = i
+        lib.gemv_gemm_q8.argtypes = [p, p, p, p, p, i, i, i, i, p]
+        lib.gemv_gemm_q8.restype = i
+        cache, batch = ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch)
+        lib.gemv_attention_workspace.argtypes = [cache, batch, i, i]
+        lib.gemv_attention_workspace.restype = z
+        lib.gemv_attention.argtypes = [cache, batch, p, i64, i, ctypes.c_float, p, p, i64, p, z, p]
+        lib.gemv_attention.restype = i
+        lib.gemv_kv_append.argtypes = [cache, batch, p, p, i64, p, i64, i, p, p, p, i64, p]
+        lib.gemv_kv_append.restype = i
+        lib.gemv_kv_evict_workspace.argtypes = [cache, batch, i]
+        lib.gemv_kv_evict_workspace.restype = z
+        lib.gemv_kv_evict.argtypes = [cache, batch, p, p, p, i64, i, i, p, p, p, p, z, p]
+        lib.gemv_kv_evict.restype = i
         _lib = lib
         return lib
 
@@ -366,3 +397,260 @@ def launch_plan_ptr(kind: str, A: int, scale: int, x: int, y: int, M: int, N: in
     """gemv_launch_plan on raw device pointers (scale 0 for FP formats)."""
     _dims(M, N)
     return load().gemv_launch_plan(KIND[kind], A, scale or None, x, y, M, N, ctypes.byref(Plan(*plan)), stream)
+
+
+# ---------------------------------------------------------------- several tokens, and the key-value cache
+# These take strided rows where the C ABI does, and make their outputs and
+# workspaces on the stream that the work runs on.
+def _work_stream(stream):
+    """(handle, maker of empty tensors) of `stream`, or of the current stream."""
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream, torch.empty
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+    def empty(*args, **kw):
+        # the allocator hands memory out by stream: what is freed when this
+        # call returns must not go to another stream while the work runs
+        with torch.cuda.stream(stream):
+            return torch.empty(*args, **kw)
+
+    return stream.cuda_stream, empty
+
+
+def _rows(t, name, dtypes, shape):
+    """Data pointer and row stride of a device tensor whose rows are dense
+    (the rows themselves may lie apart)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.is_contiguous():
+        _need(t, name, dtypes, shape)
+        return t.data_ptr(), t[0].numel() if t.shape[0] else max(1, t.stride(0))
+    if t.dim() < 2 or t.stride(0) < 0 or not (t.shape[0] == 0 or t[0].is_contiguous()):
+        raise ValueError(f"{name}: the rows must be contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a tensor of the current device, not of {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _code(dtype):
+    code = DTYPE.get(str(dtype)[6:])
+    if code is None:
+        raise TypeError(f"dtype {dtype} is none of {sorted(DTYPE)}")
+    return code
+
+
+def quantize_tokens_q8_ptr(x: int, dtype: int, stride: int, q: int, scale: int, T: int, N: int, stream: int = 0) -> int:
+    return load().gemv_quantize_tokens_q8(x, dtype, stride, q, scale, T, N, stream)
+
+
+def gemm_q8_ptr(A: int, scale: int, x: int, x_scale: int, y: int, dtype: int, T: int, M: int, N: int,
+                stream: int = 0) -> int:
+    return load().gemv_gemm_q8(A, scale, x, x_scale, y, dtype, T, M, N, stream)
+
+
+def quantize_tokens_q8(x, stream=None):
+    """Activations x [T, N] (float32, float16 or bfloat16; rows may lie apart)
+    -> (q int8 [T, N], scale float32 [T]), one scale per token."""
+    import torch
+
+    T, N = x.shape
+    _dims(T, N)
+    xp, stride = _rows(x, "x", (torch.float32, torch.float16, torch.bfloat16), (T, N))
+    handle, empty = _work_stream(stream)
+    q = empty((T, N), dtype=torch.int8, device=x.device)
+    s = empty(T, dtype=torch.float32, device=x.device)
+    _check(quantize_tokens_q8_ptr(xp, _code(x.dtype), stride, q.data_ptr(), s.data_ptr(), T, N, handle),
+           "gemv_quantize_tokens_q8")
+    return q, s
+
+
+def gemm_q8(A, scale, x, x_scale, out=None, out_dtype=None, stream=None):
+    """The INT8 product of several tokens: A int8 [M, N] with scale float16 [M]
+    (the weights of gemv_q8), x int8 [T, N] with x_scale float32 [T] ->
+    y [T, M] of `out_dtype` (float16 unless given, or `out`'s)."""
+    import torch
+
+    M, N = A.shape
+    T = x.shape[0]
+    _dims(T, M, N)
+    a = _need(A, "A", (torch.int8,), (M, N))
+    s = _need(scale, "scale", (torch.float16, torch.int16, torch.uint16), (M,))
+    xp = _need(x, "x", (torch.int8,), (T, N))
+    xs = _need(x_scale, "x_scale", (torch.float32,), (T,))
+    handle, empty = _work_stream(stream)
+    if out is None:
+        out = empty((T, M), dtype=out_dtype or torch.float16, device=A.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    dtype = _code(out.dtype)
+    y = _need(out, "out", (out.dtype,), (T, M))
+    _check(gemm_q8_ptr(a, s, xp, xs, y, dtype, T, M, N, handle), "gemv_gemm_q8")
+    return out
+
+
+class PagedCache:
+    """A paged key-value cache: k and v [pages, page_size, heads, head_dim],
+    float16 or bfloat16, the last dimension dense and the others in any order
+    in memory, the same for both (so a cache kept as [pages, heads, page_size,
+    head_dim] is given as ``t.transpose(1, 2)``).  Keeps the tensors; their
+    contents belong to the caller."""
+
+    def __init__(self, k, v):
+        import torch
+
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a device tensor")
+            if t.dtype not in (torch.float16, torch.bfloat16):
+                raise TypeError(f"{name}: dtype {t.dtype} is neither float16 nor bfloat16")
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be [pages, page_size, heads, head_dim]")
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must have the same shape, type and device")
+        pages, page_size, heads, dim = k.shape
+        _dims(pages, page_size, heads, dim)
+        if page_size < 1 or heads < 1:
+            raise ValueError("a page holds at least one slot of at least one head")
+        if dim < 8 or dim > 256 or dim % 8:
+            raise ValueError(f"head_dim {dim} is no multiple of 8 from 8 to 256")
+        # a dimension of size 1 is never stepped over: its stride is free
+        strides = [tuple(max(t.stride(d), dim) if t.shape[d] == 1 else t.stride(d) for d in range(3)) for t in (k, v)]
+        if strides[0] != strides[1]:
+            raise ValueError("k and v must have the same strides")
+        if k.stride(3) != 1 or v.stride(3) != 1 or min(strides[0]) < dim:
+            raise ValueError("the last dimension must be dense and rows must not overlap")
+        if any(s % 8 for s in strides[0]) or k.data_ptr() % 16 or v.data_ptr() % 16:
+            raise ValueError("k, v and their rows must be 16-byte aligned")
+        self.k, self.v = k, v
+        self.pages, self.page_size, self.heads, self.head_dim = pages, page_size, heads, dim
+        self.dtype, self.device = k.dtype, k.device
+        self.c = KvCache(k.data_ptr(), v.data_ptr(), _code(k.dtype), pages, page_size, heads, dim, *strides[0])
+
+    def _batch(self, table, lens, max_len):
+        """gemv_kv_batch of a call, and the slots that its sequences may use."""
+        import torch
+
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
+        B, width = table.shape
+        tp, stride = _rows(table, "table", (torch.int32,), (B, width))
+        lp = _need(lens, "lens", (torch.int32,), (B,))
+        room = min(width * self.page_size, _INT_MAX)
+        if max_len is None:
+            max_len = room
+        if not 0 <= max_len <= _INT_MAX:
+            raise ValueError(f"max_len {max_len} outside [0, 2^31 - 1]")
+        return KvBatch(tp, max(stride, width), width, lp, B, max_len), min(room, max_len)
+
+
+def _tracked(t, name, dtype, batch, heads, room):
+    if t.dim() != 3 or t.shape[2] < room:
+        raise ValueError(f"{name} must be [batch, heads, slots] with at least {room} slots")
+    return _need(t, name, (dtype,), (batch, heads, t.shape[2]))
+
+
+def paged_attention(cache, table, lens, q, scale=None, max_len=None, weights=None, out=None, stream=None):
+    """Attention of one new token per sequence over a paged cache: q
+    [batch, q_heads, head_dim] of the cache's type (sequences may lie apart)
+    -> [batch, q_heads, head_dim].  table int32 [batch, pages per sequence],
+    lens int32 [batch]; scale 1 / sqrt(head_dim) unless given; max_len the
+    longest length, where the host knows one below the table's room.
+    weights float32 [batch, heads, slots]: each token's attention weights,
+    summed over the query heads of its head, are added to it."""
+    import torch
+
+    batch, room = cache._batch(table, lens, max_len)
+    B, heads, dim = q.shape
+    if B != batch.batch or dim != cache.head_dim or heads < 1 or heads % cache.heads:
+        raise ValueError(f"q: shape {tuple(q.shape)} does not fit {batch.batch} sequences, {cache.heads} heads of "
+                         f"{cache.head_dim}")
+    qp, q_stride = _rows(q, "q", (cache.dtype,), (B, heads, dim))
+    handle, empty = _work_stream(stream)
+    if out is None:
+        out = empty((B, heads, dim), dtype=cache.dtype, device=q.device)
+    op = _need(out, "out", (cache.dtype,), (B, heads, dim))
+    wp = None if weights is None else _tracked(weights, "weights", torch.float32, B, cache.heads, room)
+    slots = 0 if weights is None else weights.shape[2]
+    scale = dim ** -0.5 if scale is None else scale
+    lib, c, s = load(), ctypes.byref(cache.c), ctypes.byref(batch)
+    need = lib.gemv_attention_workspace(c, s, heads, wp is not None)
+    work = empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _check(lib.gemv_attention(c, s, qp, max(q_stride, heads * dim), heads, scale, op, wp, slots,
+                              work.data_ptr() if need else None, need, handle), "gemv_attention")
+    return out
+
+
+def kv_append(cache, table, lens, starts, k, v, weights=None, positions=None, seen=None, stream=None):
+    """Writes new tokens to a paged cache: rows starts[b] .. starts[b+1] - 1 of
+    k and v [rows, heads, head_dim] (rows may lie apart) become the last tokens
+    of sequence b, which with them holds lens[b].  starts int32 [batch + 1].
+    With weights float32 and positions int32 [batch, heads, slots] and seen
+    int32 [batch], the slots' weights become 0 and their positions those of
+    the sequence's last tokens, of seen[b] in all."""
+    import torch
+
+    batch, room = cache._batch(table, lens, None)
+    B, rows = batch.batch, k.shape[0]
+    _dims(rows)
+    shape = (rows, cache.heads, cache.head_dim)
+    kp, k_stride = _rows(k, "k", (cache.dtype,), shape)
+    vp, v_stride = _rows(v, "v", (cache.dtype,), shape)
+    sp = _need(starts, "starts", (torch.int32,), (B + 1,))
+    if len({weights is None, positions is None, seen is None}) != 1:
+        raise ValueError("weights, positions and seen go together")
+    wp = pp = np = None
+    slots = 0
+    if weights is not None:
+        slots = weights.shape[-1]
+        wp = _tracked(weights, "weights", torch.float32, B, cache.heads, 0)
+        pp = _need(positions, "positions", (torch.int32,), (B, cache.heads, slots))
+        np = _need(seen, "seen", (torch.int32,), (B,))
+    handle, _ = _work_stream(stream)
+    width = cache.heads * cache.head_dim
+    _check(load().gemv_kv_append(ctypes.byref(cache.c), ctypes.byref(batch), sp, kp, max(k_stride, width), vp,
+                                 max(v_stride, width), rows, wp, pp, np, slots, handle), "gemv_kv_append")
+
+
+def kv_evict(cache, table, lens, seen, weights, positions, budget, recent, max_len=None, out=None, stream=None):
+    """Evicts from a paged cache by accumulated attention weight: each head of
+    a sequence over `budget` keeps its tokens of the last `recent` positions
+    and of the others those of the largest weight, `budget` in all; keys and
+    values move in place.  weights float32 and positions int32 [batch, heads,
+    slots], seen int32 [batch] (see kv_append).  Returns, or writes to
+    ``out``, (weights, positions, lens) afterwards."""
+    import torch
+
+    batch, room = cache._batch(table, lens, max_len)
+    B = batch.batch
+    wp = _tracked(weights, "weights", torch.float32, B, cache.heads, room)
+    slots = weights.shape[2]
+    pp = _need(positions, "positions", (torch.int32,), (B, cache.heads, slots))
+    np = _need(seen, "seen", (torch.int32,), (B,))
+    _dims(budget, recent)
+    handle, empty = _work_stream(stream)
+    if out is None:
+        out = (empty(weights.shape, dtype=torch.float32, device=weights.device),
+               empty(weights.shape, dtype=torch.int32, device=weights.device),
+               empty(B, dtype=torch.int32, device=weights.device))
+    new_w, new_p, left = out
+    outs = (_need(new_w, "out[0]", (torch.float32,), weights.shape), _need(new_p, "out[1]", (torch.int32,), weights.shape),
+            _need(left, "out[2]", (torch.int32,), (B,)))
+    if weights.numel() and (outs[0] == wp or outs[1] == pp) or B and outs[2] == batch.lens:
+        raise ValueError("the outputs must not be the inputs")
+    lib, c, s = load(), ctypes.byref(cache.c), ctypes.byref(batch)
+    need = lib.gemv_kv_evict_workspace(c, s, budget)
+    work = empty(max(need, 16), dtype=torch.uint8, device=weights.device)
+    _check(lib.gemv_kv_evict(c, s, np, wp, pp, slots, budget, recent, *outs, work.data_ptr(), need, handle),
+           "gemv_kv_evict")
+    return new_w, new_p, left

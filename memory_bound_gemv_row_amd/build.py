@@ -1,9 +1,11 @@
 """Build the gfx950 HIP library in-tree with hipcc.
 
 ``python -m memory_bound_gemv_row_amd.build`` compiles
-``csrc/gemv_api.hip`` (GEMV, which includes its kernels) and
-``csrc/quant_api.hip`` (the weight quantiser) and ``csrc/softmax_api.hip``
-(the row softmax) into one library,
+``csrc/gemv_api.hip`` (GEMV, which includes its kernels),
+``csrc/quant_api.hip`` (the weight quantiser), ``csrc/softmax_api.hip``
+(the row softmax), ``csrc/tokens_api.hip`` (the INT8 product of several
+tokens) and ``csrc/attention_api.hip`` (attention over a paged key-value
+cache and the cache's upkeep) into one library,
 ``memory_bound_gemv_row_amd/libgemv_amd.so``.
 """
 from __future__ import annotations
@@ -17,10 +19,12 @@ ROOT = os.path.dirname(PKG)
 SRC_DIR = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemv_amd.so")
-SOURCES = [os.path.join(SRC_DIR, f) for f in ("gemv_api.hip", "quant_api.hip", "softmax_api.hip")]
+SOURCES = [os.path.join(SRC_DIR, f) for f in ("gemv_api.hip", "quant_api.hip", "softmax_api.hip", "tokens_api.hip",
+                                                 "attention_api.hip")]
 DEPENDS = SOURCES + [os.path.join(SRC_DIR, f) for f in ("gemv_kernels.hpp", "quant_kernels.hpp", "softmax_kernels.hpp",
-                                                    "device_info.hpp")] \
-    + [os.path.join(INCLUDE, f) for f in ("gemv.h", "gemv_quant.h", "gemv_softmax.h")]
+                                                    "tokens_kernels.hpp", "attention_kernels.hpp", "device_info.hpp")] \
+    + [os.path.join(INCLUDE, f) for f in ("gemv.h", "gemv_quant.h", "gemv_softmax.h", "gemv_types.h", "gemv_tokens.h",
+                                             "gemv_attention.h")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

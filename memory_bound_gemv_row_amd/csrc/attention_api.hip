@@ -1,0 +1,300 @@
+// attention_api.hip -- C ABI of decode attention over a paged key-value cache,
+// its append and its eviction (declared in include/gemv_attention.h):
+// validation, workspaces, geometry and launch.
+#include "gemv_attention.h"
+#include "attention_kernels.hpp"
+#include "device_info.hpp"
+
+#include <hip/hip_runtime.h>
+
+#include <limits.h>
+
+namespace gattn {
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+Divider divider(int d)
+{
+    unsigned shift = 0;
+    while (((uint64_t)1 << shift) < (uint64_t)d)
+        ++shift;
+    const uint64_t over = ((uint64_t)1 << shift) - (uint64_t)d;
+    return Divider{(unsigned)((over << 32) / (uint64_t)d + 1), shift};
+}
+
+// Checks shared by every entry point; fills the addressing part.
+int check(const gemv_kv_cache* c, const gemv_kv_batch* s, Pages* out)
+{
+    if (c == nullptr || s == nullptr)
+        return GEMV_E_INVAL;
+    if (s->batch < 0 || s->width < 0 || s->max_len < 0 || s->table_stride < s->width)
+        return GEMV_E_INVAL;
+    if (c->pages < 0 || c->page_size < 1 || c->heads < 1 || c->head_dim < 1 ||
+        (c->dtype != GEMV_F16 && c->dtype != GEMV_BF16))
+        return GEMV_E_INVAL;
+    if (c->stride_page < c->head_dim || c->stride_slot < c->head_dim || c->stride_head < c->head_dim)
+        return GEMV_E_INVAL;
+    if (s->batch > 0 && s->lens == nullptr)
+        return GEMV_E_INVAL;
+    if (s->batch > 0 && s->width > 0 && (s->table == nullptr || (c->pages > 0 && (c->k == nullptr || c->v == nullptr))))
+        return GEMV_E_INVAL;
+    if (c->head_dim % 8 != 0 || c->head_dim > 256 || c->stride_page % 8 != 0 || c->stride_slot % 8 != 0 ||
+        c->stride_head % 8 != 0 || !aligned(c->k, 16) || !aligned(c->v, 16))
+        return GEMV_E_UNSUPPORTED;
+    const int64_t room = (int64_t)s->width * c->page_size;
+    const int64_t limit = room < s->max_len ? room : s->max_len;
+    *out = Pages{s->table, s->table_stride, s->lens, (int)limit, c->pages, c->page_size, divider(c->page_size),
+                 c->stride_page, c->stride_slot, c->stride_head};
+    return GEMV_OK;
+}
+
+int launch(const void* fn, int64_t grid, int block, void** args, hipStream_t stream)
+{
+    return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(block), args, 0, stream) == hipSuccess ? GEMV_OK
+                                                                                                 : GEMV_E_LAUNCH;
+}
+
+bool fits(int64_t grid, int block) { return grid <= gemv_device::kMaxWorkItems / block; }
+
+// How the length is split: workgroups per key-value head and slots of each.
+struct Split {
+    int tiles, parts, chunk;
+    size_t ms_at, out_at, logits_at, bytes;
+};
+
+Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q_heads, bool weighted, int cus)
+{
+    Split p;
+    const int group = q_heads / c->heads;
+    p.tiles = (group + 15) / 16;
+    const int64_t items = (int64_t)s->batch * c->heads * p.tiles;
+    const int64_t most = ((int64_t)limit + 255) / 256;   // no part below 256 slots
+    int64_t parts = items > 0 ? ((int64_t)cus * 4 + items - 1) / items : 1;
+    parts = parts < most ? parts : most;
+    parts = parts < 1 ? 1 : parts;
+    const int64_t chunk = (((int64_t)limit + parts - 1) / parts + 63) / 64 * 64;
+    p.chunk = (int)(chunk < 64 ? 64 : (chunk > (1 << 30) ? (1 << 30) : chunk));
+    p.parts = (int)(((int64_t)limit + p.chunk - 1) / p.chunk);
+    p.parts = p.parts < 1 ? 1 : p.parts;
+    const size_t rows = (size_t)s->batch * (size_t)q_heads;
+    p.ms_at = 0;
+    p.out_at = p.parts > 1 || weighted ? round16(rows * p.parts * 2 * sizeof(float)) : 0;
+    p.logits_at = p.out_at + (p.parts > 1 ? round16(rows * p.parts * c->head_dim * sizeof(float)) : 0);
+    p.bytes = p.logits_at + (weighted ? round16(rows * limit * sizeof(float)) : 0);
+    return p;
+}
+
+template <int DT>
+const void* attention_for(int dim)
+{
+    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64>)
+           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128>)
+                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256>);
+}
+
+int evict_moves(int limit, int budget)
+{
+    const int over = limit > budget ? limit - budget : 0;
+    return over < budget ? over : budget;
+}
+
+size_t evict_bytes(int batch, int heads, int moves)
+{
+    const size_t bh = (size_t)batch * (size_t)heads;
+    return round16(bh * sizeof(int32_t)) + bh * 2 * (size_t)moves * sizeof(int32_t);
+}
+
+}  // namespace
+}  // namespace gattn
+
+extern "C" {
+
+size_t gemv_attention_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* batch, int q_heads, int weighted)
+{
+    using namespace gattn;
+    Pages at{};
+    if (check(cache, batch, &at) != GEMV_OK || q_heads < 1 || q_heads % cache->heads != 0)
+        return 0;
+    gemv_device::Device dev{};
+    if (gemv_device::current(&dev) != GEMV_OK)
+        return 0;
+    return split_for(cache, batch, at.limit, q_heads, weighted != 0, dev.cus).bytes;
+}
+
+int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const void* q, int64_t q_stride,
+                   int q_heads, float scale, void* out, float* weights, int64_t slots, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream)
+{
+    using namespace gattn;
+    Attention a{};
+    if (int rc = check(cache, batch, &a.at); rc != GEMV_OK)
+        return rc;
+    if (q_heads < 1 || q_heads % cache->heads != 0 || (weights != nullptr && slots < a.at.limit) ||
+        q_stride < (int64_t)q_heads * cache->head_dim)
+        return GEMV_E_INVAL;
+    if (batch->batch == 0)
+        return GEMV_OK;
+    if (q == nullptr || out == nullptr)
+        return GEMV_E_INVAL;
+    if (q_stride % 8 != 0 || !aligned(q, 16) || !aligned(out, 2))
+        return GEMV_E_UNSUPPORTED;
+    gemv_device::Device dev{};
+    if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
+        return rc;
+    const Split p = split_for(cache, batch, a.at.limit, q_heads, weights != nullptr, dev.cus);
+    if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes || !aligned(workspace, 16)))
+        return GEMV_E_INVAL;
+    const int64_t items = (int64_t)batch->batch * cache->heads;
+    const int64_t grid = items * p.tiles * p.parts;
+    int blocks = (int)(((int64_t)a.at.limit + 255) / 256);
+    if (!fits(grid, kWaves * 64) || !fits((int64_t)batch->batch * q_heads, 128) ||
+        (weights != nullptr && !fits(items * blocks, 256)))
+        return GEMV_E_UNSUPPORTED;
+    char* ws = static_cast<char*>(workspace);
+    a.k = static_cast<const uint16_t*>(cache->k);
+    a.v = static_cast<const uint16_t*>(cache->v);
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_stride = q_stride;
+    a.q_heads = q_heads;
+    a.heads = cache->heads;
+    a.dim = cache->head_dim;
+    a.group = q_heads / cache->heads;
+    a.tiles = p.tiles;
+    a.parts = p.parts;
+    a.chunk = p.chunk;
+    a.scale = scale * 1.44269504088896340736f;
+    a.out = out;
+    a.part_ms = p.parts > 1 || weights != nullptr ? reinterpret_cast<float*>(ws + p.ms_at) : nullptr;
+    a.part_out = p.parts > 1 ? reinterpret_cast<float*>(ws + p.out_at) : nullptr;
+    a.logits = weights != nullptr ? reinterpret_cast<float*>(ws + p.logits_at) : nullptr;
+    a.weights = weights;
+    a.slots = slots;
+    void* args[] = {(void*)&a};
+    const bool half = cache->dtype == GEMV_F16;
+    if (int rc = launch(half ? attention_for<kF16>(a.dim) : attention_for<kBF16>(a.dim), grid, kWaves * 64, args, stream);
+        rc != GEMV_OK)
+        return rc;
+    if (p.parts > 1) {
+        const void* fn = half ? reinterpret_cast<const void*>(&join_kernel<kF16>)
+                              : reinterpret_cast<const void*>(&join_kernel<kBF16>);
+        if (int rc = launch(fn, (int64_t)batch->batch * q_heads, 128, args, stream); rc != GEMV_OK)
+            return rc;
+    }
+    if (weights != nullptr && blocks > 0) {
+        void* wargs[] = {(void*)&a, (void*)&blocks};
+        return launch(reinterpret_cast<const void*>(&weights_kernel), items * blocks, 256, wargs, stream);
+    }
+    return GEMV_OK;
+}
+
+int gemv_kv_append(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* starts, const void* k,
+                   int64_t k_stride, const void* v, int64_t v_stride, int rows, float* weights, int32_t* positions,
+                   const int32_t* seen, int64_t slots, hipStream_t stream)
+{
+    using namespace gattn;
+    Append a{};
+    if (cache == nullptr || batch == nullptr)
+        return GEMV_E_INVAL;
+    gemv_kv_batch all = *batch;
+    all.max_len = INT_MAX;
+    if (int rc = check(cache, &all, &a.at); rc != GEMV_OK)
+        return rc;
+    const int64_t width = (int64_t)cache->heads * cache->head_dim;
+    if (rows < 0 || k_stride < width || v_stride < width)
+        return GEMV_E_INVAL;
+    const int tracked = (weights != nullptr) + (positions != nullptr) + (seen != nullptr);
+    if ((tracked != 0 && tracked != 3) || (tracked == 3 && slots < 0))
+        return GEMV_E_INVAL;
+    if (batch->batch == 0 || rows == 0 || a.at.limit == 0)
+        return GEMV_OK;
+    if (starts == nullptr || k == nullptr || v == nullptr)
+        return GEMV_E_INVAL;
+    if (k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(k, 16) || !aligned(v, 16))
+        return GEMV_E_UNSUPPORTED;
+    gemv_device::Device dev{};
+    if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
+        return rc;
+    a.k = static_cast<uint16_t*>(cache->k);
+    a.v = static_cast<uint16_t*>(cache->v);
+    a.starts = starts;
+    a.new_k = static_cast<const uint16_t*>(k);
+    a.new_v = static_cast<const uint16_t*>(v);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.rows = rows;
+    a.batch = batch->batch;
+    a.heads = cache->heads;
+    a.dim = cache->head_dim;
+    a.weights = weights;
+    a.positions = positions;
+    a.seen = seen;
+    a.slots = slots;
+    void* args[] = {(void*)&a};
+    return launch(reinterpret_cast<const void*>(&append_kernel), gemv_device::capped_grid(((int64_t)rows + 3) / 4, 256),
+                  256, args, stream);
+}
+
+size_t gemv_kv_evict_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* batch, int budget)
+{
+    using namespace gattn;
+    Pages at{};
+    if (check(cache, batch, &at) != GEMV_OK || budget < 0)
+        return 0;
+    return evict_bytes(batch->batch, cache->heads, evict_moves(at.limit, budget));
+}
+
+int gemv_kv_evict(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* seen, const float* weights,
+                  const int32_t* positions, int64_t slots, int budget, int recent, float* weights_out,
+                  int32_t* positions_out, int32_t* lens_out, void* workspace, size_t workspace_bytes,
+                  hipStream_t stream)
+{
+    using namespace gattn;
+    Evict a{};
+    if (int rc = check(cache, batch, &a.at); rc != GEMV_OK)
+        return rc;
+    if (budget < 0 || recent < 0 || slots < a.at.limit)
+        return GEMV_E_INVAL;
+    if (batch->batch == 0)
+        return GEMV_OK;
+    if (seen == nullptr || lens_out == nullptr ||
+        (slots > 0 && (weights == nullptr || positions == nullptr || weights_out == nullptr || positions_out == nullptr)))
+        return GEMV_E_INVAL;
+    gemv_device::Device dev{};
+    if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
+        return rc;
+    a.moves_max = evict_moves(a.at.limit, budget);
+    const size_t bytes = evict_bytes(batch->batch, cache->heads, a.moves_max);
+    if (workspace == nullptr || workspace_bytes < bytes || !aligned(workspace, 16))
+        return GEMV_E_INVAL;
+    const int64_t items = (int64_t)batch->batch * cache->heads;
+    int blocks = (a.moves_max + 31) / 32;   // eight moves a wave
+    blocks = blocks > 256 ? 256 : blocks;
+    if (!fits(items, kEvictThreads) || !fits(items * blocks, 256))
+        return GEMV_E_UNSUPPORTED;
+    a.k = static_cast<uint16_t*>(cache->k);
+    a.v = static_cast<uint16_t*>(cache->v);
+    a.seen = seen;
+    a.weights = weights;
+    a.positions = positions;
+    a.slots = slots;
+    a.heads = cache->heads;
+    a.dim = cache->head_dim;
+    a.budget = budget;
+    a.recent = recent;
+    a.weights_out = weights_out;
+    a.positions_out = positions_out;
+    a.lens_out = lens_out;
+    a.count = static_cast<int32_t*>(workspace);
+    a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + round16((size_t)items * sizeof(int32_t)));
+    void* args[] = {(void*)&a};
+    if (int rc = launch(reinterpret_cast<const void*>(&evict_select_kernel), items, kEvictThreads, args, stream);
+        rc != GEMV_OK || blocks == 0)
+        return rc;
+    void* margs[] = {(void*)&a, (void*)&blocks};
+    return launch(reinterpret_cast<const void*>(&evict_move_kernel), items * blocks, 256, margs, stream);
+}
+
+}  // extern "C"
