@@ -62,37 +62,56 @@ bool fits(int64_t grid, int block) { return grid <= gemv_device::kMaxWorkItems /
 // How the length is split: workgroups per key-value head and slots of each.
 struct Split {
     int tiles, parts, chunk;
+    int64_t logits_stride;
     size_t ms_at, out_at, logits_at, bytes;
 };
 
+// The length is cut into parts so that there are about four workgroups per
+// CU, of 64 slots (a tile for each wave) to 1024: where lengths are ragged,
+// short parts even out what the CUs get.
 Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q_heads, bool weighted, int cus)
 {
     Split p;
     const int group = q_heads / c->heads;
     p.tiles = (group + 15) / 16;
     const int64_t items = (int64_t)s->batch * c->heads * p.tiles;
-    const int64_t most = ((int64_t)limit + 255) / 256;   // no part below 256 slots
-    int64_t parts = items > 0 ? ((int64_t)cus * 4 + items - 1) / items : 1;
-    parts = parts < most ? parts : most;
-    parts = parts < 1 ? 1 : parts;
-    const int64_t chunk = (((int64_t)limit + parts - 1) / parts + 63) / 64 * 64;
-    p.chunk = (int)(chunk < 64 ? 64 : (chunk > (1 << 30) ? (1 << 30) : chunk));
+    int64_t chunk = items > 0 ? (int64_t)limit * items / ((int64_t)cus * 4) : limit;
+    chunk = (chunk + 63) / 64 * 64;
+    chunk = chunk < 64 ? 64 : (chunk > 1024 ? 1024 : chunk);
+    p.chunk = (int)chunk;
     p.parts = (int)(((int64_t)limit + p.chunk - 1) / p.chunk);
     p.parts = p.parts < 1 ? 1 : p.parts;
     const size_t rows = (size_t)s->batch * (size_t)q_heads;
     p.ms_at = 0;
     p.out_at = p.parts > 1 || weighted ? round16(rows * p.parts * 2 * sizeof(float)) : 0;
     p.logits_at = p.out_at + (p.parts > 1 ? round16(rows * p.parts * c->head_dim * sizeof(float)) : 0);
-    p.bytes = p.logits_at + (weighted ? round16(rows * limit * sizeof(float)) : 0);
+    p.logits_stride = ((int64_t)limit + 15) / 16 * 16;
+    p.bytes = p.logits_at + (weighted ? rows * (size_t)p.logits_stride * sizeof(float) : 0);
     return p;
 }
 
-template <int DT>
-const void* attention_for(int dim)
+template <int DT, bool WHOLE>
+const void* attention_sized(int dim)
 {
-    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64>)
-           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128>)
-                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256>);
+    if constexpr (WHOLE) {
+        if (dim == 64)
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 64, true, true>);
+        if (dim == 128)
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 128, true, true>);
+        if (dim == 256)
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 256, true, true>);
+    }
+    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64, WHOLE, false>)
+           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128, WHOLE, false>)
+                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256, WHOLE, false>);
+}
+
+const void* attention_for(const gemv_kv_cache* c)
+{
+    const bool whole = c->page_size % 16 == 0 && c->stride_slot < (1 << 26);
+    if (c->dtype == GEMV_F16)
+        return whole ? attention_sized<kF16, true>(c->head_dim) : attention_sized<kF16, false>(c->head_dim);
+    return whole ? attention_sized<kBF16, true>(c->head_dim) : attention_sized<kBF16, false>(c->head_dim);
 }
 
 int evict_moves(int limit, int budget)
@@ -149,9 +168,9 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
         return GEMV_E_INVAL;
     const int64_t items = (int64_t)batch->batch * cache->heads;
     const int64_t grid = items * p.tiles * p.parts;
-    int blocks = (int)(((int64_t)a.at.limit + 255) / 256);
-    if (!fits(grid, kWaves * 64) || !fits((int64_t)batch->batch * q_heads, 128) ||
-        (weights != nullptr && !fits(items * blocks, 256)))
+    const int64_t joins = p.parts > 1 ? (int64_t)batch->batch * q_heads : 0;
+    int blocks = weights != nullptr ? (int)(((int64_t)a.at.limit + 1023) / 1024) : 0;
+    if (!fits(grid, kWaves * 64) || !fits(joins + items * blocks, 256))
         return GEMV_E_UNSUPPORTED;
     char* ws = static_cast<char*>(workspace);
     a.k = static_cast<const uint16_t*>(cache->k);
@@ -170,24 +189,19 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
     a.part_ms = p.parts > 1 || weights != nullptr ? reinterpret_cast<float*>(ws + p.ms_at) : nullptr;
     a.part_out = p.parts > 1 ? reinterpret_cast<float*>(ws + p.out_at) : nullptr;
     a.logits = weights != nullptr ? reinterpret_cast<float*>(ws + p.logits_at) : nullptr;
+    a.logits_stride = p.logits_stride;
     a.weights = weights;
     a.slots = slots;
     void* args[] = {(void*)&a};
-    const bool half = cache->dtype == GEMV_F16;
-    if (int rc = launch(half ? attention_for<kF16>(a.dim) : attention_for<kBF16>(a.dim), grid, kWaves * 64, args, stream);
-        rc != GEMV_OK)
+    if (int rc = launch(attention_for(cache), grid, kWaves * 64, args, stream); rc != GEMV_OK)
         return rc;
-    if (p.parts > 1) {
-        const void* fn = half ? reinterpret_cast<const void*>(&join_kernel<kF16>)
-                              : reinterpret_cast<const void*>(&join_kernel<kBF16>);
-        if (int rc = launch(fn, (int64_t)batch->batch * q_heads, 128, args, stream); rc != GEMV_OK)
-            return rc;
-    }
-    if (weights != nullptr && blocks > 0) {
-        void* wargs[] = {(void*)&a, (void*)&blocks};
-        return launch(reinterpret_cast<const void*>(&weights_kernel), items * blocks, 256, wargs, stream);
-    }
-    return GEMV_OK;
+    if (joins + items * blocks == 0)
+        return GEMV_OK;
+    int rows = (int)joins;
+    void* jargs[] = {(void*)&a, (void*)&rows, (void*)&blocks};
+    return launch(cache->dtype == GEMV_F16 ? reinterpret_cast<const void*>(&join_kernel<kF16>)
+                                           : reinterpret_cast<const void*>(&join_kernel<kBF16>),
+                  joins + items * blocks, 256, jargs, stream);
 }
 
 int gemv_kv_append(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* starts, const void* k,

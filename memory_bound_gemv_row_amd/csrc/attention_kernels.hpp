@@ -101,13 +101,29 @@ struct Attention {
     void* out;
     float* part_out;  // [batch][q_heads][parts][dim], not divided by the sums
     float* part_ms;   // [batch][q_heads][parts][2]: maximum and sum of powers
-    float* logits;    // [batch][q_heads][limit], or null
+    float* logits;    // [batch][q_heads][logits_stride], or null
+    int64_t logits_stride;   // the longest length in whole tiles
     float* weights;   // [batch][heads][slots], or null
     int64_t slots;
 };
 
+// What brings a part's sums to the common maximum `top`.  An empty part has
+// maximum -inf and sum 0; one whose sum is NaN under a maximum of -inf stays NaN.
+__device__ __forceinline__ float part_factor(float m, float s, float top)
+{
+    return m == -kInf ? (s == 0.0f ? 0.0f : 1.0f) : exp2_hw(m - top);
+}
+
 constexpr int kWaves = 4;
 constexpr float kSlack = 8.0f;   // powers of two that a logit may pass the reference maximum by
+
+__device__ __forceinline__ const uint16_t* uniform(const uint16_t* p)
+{
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)u);
+    const unsigned hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(u >> 32));
+    return reinterpret_cast<const uint16_t*>((uint64_t)hi << 32 | lo);
+}
 
 // One workgroup: up to 16 query heads of one key-value head of one sequence,
 // over one part of its length.  Its waves take tiles of 16 slots in turn.
@@ -125,7 +141,14 @@ constexpr float kSlack = 8.0f;   // powers of two that a logit may pass the refe
 // then stay below 2^kSlack, which binary32 sums hold as exactly as those
 // below 1, and the sums are rescaled a few times per sequence instead of
 // with each tile.
-template <int DT, int DP>
+//
+// A wave loads its next tile while it multiplies the current one.  Where
+// pages are whole numbers of tiles (WHOLE), a tile has one page: its address
+// is the same for all lanes, and one load per 64 tiles brings the page
+// numbers.  Otherwise each lane looks its key's slot up a tile ahead, and the
+// addresses of the values come from the lanes that hold those keys.  EXACT:
+// the head's size is DP, so no lane is without an element.
+template <int DT, int DP, bool WHOLE, bool EXACT>
 __global__ void __launch_bounds__(kWaves * 64)
 attention_kernel(Attention a)
 {
@@ -147,9 +170,11 @@ attention_kernel(Attention a)
     item /= a.tiles;
     const int kv = item % a.heads;
     const int b = item / a.heads;
-    const int len = a.at.length(b);
+    const int len = __builtin_amdgcn_readfirstlane(a.at.length(b));
     const int64_t first = (int64_t)part * a.chunk;
-    const int begin = first < len ? (int)first : len;
+    if (part > 0 && first >= len)
+        return;                                                          // the join does not look at it
+    const int begin = (int)first;
     const int end = first + a.chunk < len ? (int)(first + a.chunk) : len;
     const int head0 = kv * a.group + tile * 16;                          // this workgroup's query heads
     const int nheads = a.group - tile * 16 < 16 ? a.group - tile * 16 : 16;
@@ -159,7 +184,7 @@ attention_kernel(Attention a)
     for (int s = 0; s < kSteps; ++s) {
         const int d = 32 * s + 8 * quarter;
         query[s] = u32x4{0, 0, 0, 0};
-        if (col < nheads && d < a.dim)
+        if (col < nheads && (EXACT || d < a.dim))
             query[s] = *reinterpret_cast<const u32x4*>(a.q + b * a.q_stride + (int64_t)(head0 + col) * a.dim + d);
     }
 
@@ -171,60 +196,139 @@ attention_kernel(Attention a)
         for (int e = 0; e < VW; ++e)
             acc[s][e] = f32x4{0, 0, 0, 0};
 
-    for (int j0 = begin + wave * 16; j0 < end; j0 += kWaves * 16) {
-        // this lane's key, and the four slots whose values it loads
-        const int jk = j0 + col;
-        const int64_t ok = jk < end ? a.at.offset(b, jk) : -1;
+    struct Tile {
         u32x4 key[kSteps];
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int d = 32 * s + 8 * quarter;
-            key[s] = u32x4{0, 0, 0, 0};
-            if (ok >= 0 && d < a.dim)
-                key[s] = *reinterpret_cast<const u32x4*>(a.k + ok + kv * a.at.stride_head + d);
-        }
         unsigned value[4][kSets][kWords];
-        bool held[4];
+        unsigned held;   // bit r: slot 4 quarter + r is there
+    };
+    const int tiles = (end - begin - wave * 16 + kWaves * 16 - 1) / (kWaves * 16);   // of this wave; <= 0: none
+    auto slot_of = [&](int t) { return begin + (wave + t * kWaves) * 16; };
+    const uint16_t* k0 = a.k + kv * a.at.stride_head;
+    const uint16_t* v0 = a.v + kv * a.at.stride_head;
+
+    auto value_load = [&](Tile& x, int r, int s, const uint16_t* p) {
+        if constexpr (VW == 8) {
+            const u32x4 t = *reinterpret_cast<const u32x4*>(p);
+            x.value[r][s][0] = t.x, x.value[r][s][1] = t.y, x.value[r][s][2] = t.z, x.value[r][s][3] = t.w;
+        } else {
+            const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+            x.value[r][s][0] = t.x, x.value[r][s][1] = t.y;
+        }
+    };
+    // WHOLE: the page of tile t of this wave, in lane t % 64; otherwise the
+    // offset of this lane's key of the tile to be loaded next
+    int pages = -1;
+    int64_t key_at = -1;
+    auto look_up = [&](int t) {
+        if constexpr (WHOLE) {
+            if ((t & 63) == 0) {
+                const int64_t j = (int64_t)begin + (wave + (int64_t)(t + lane) * kWaves) * 16;
+                pages = j < end ? a.at.table[b * a.at.table_stride + a.at.page_of.by((int)j)] : -1;
+            }
+        } else {
+            const int64_t j = (int64_t)begin + (wave + (int64_t)t * kWaves) * 16 + col;
+            key_at = j < end ? a.at.offset(b, (int)j) : -1;
+        }
+    };
+    // byte offsets of this lane's pieces from the tile's first slot (WHOLE;
+    // the host has checked that 16 slots span less than 2^31 bytes)
+    const unsigned key_lane = (unsigned)(col * (int)a.at.stride_slot + 8 * quarter) * 2;
+    const unsigned value_lane = (unsigned)(4 * quarter * (int)a.at.stride_slot + VW * col) * 2;
+    const unsigned value_step = (unsigned)a.at.stride_slot * 2;
+
+    auto load = [&](Tile& x, int t) {
+        if constexpr (WHOLE) {
+            const int page = __builtin_amdgcn_readlane(pages, t & 63);
+            x.held = 0;
+            if ((unsigned)page >= (unsigned)a.at.pages)
+                return;                         // past the end, or a hole: neither loaded nor used
+            const int j = slot_of(t);
+            const int i = j - a.at.page_of.by(j) * a.at.page_size;
+            const int64_t at = page * a.at.stride_page + (int64_t)i * a.at.stride_slot;
+            const char* kp = reinterpret_cast<const char*>(uniform(k0 + at));
+            const char* vp = reinterpret_cast<const char*>(uniform(v0 + at));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int j = j0 + 4 * quarter + r;
-            const int64_t ov = j < end ? a.at.offset(b, j) : -1;
-            held[r] = ov >= 0;
+            for (int s = 0; s < kSteps; ++s) {
+                if (EXACT || 32 * s + 8 * quarter < a.dim)
+                    x.key[s] = *reinterpret_cast<const u32x4*>(kp + (key_lane + 64 * s));
+                else
+                    x.key[s] = u32x4{0, 0, 0, 0};
+            }
 #pragma unroll
-            for (int s = 0; s < kSets; ++s) {
-                const int d = 16 * VW * s + VW * col;
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int w = 0; w < kWords; ++w)
-                    value[r][s][w] = 0;
-                if (held[r] && d < a.dim) {
-                    const uint16_t* p = a.v + ov + kv * a.at.stride_head + d;
-                    if constexpr (VW == 8) {
-                        const u32x4 t = *reinterpret_cast<const u32x4*>(p);
-                        value[r][s][0] = t.x, value[r][s][1] = t.y, value[r][s][2] = t.z, value[r][s][3] = t.w;
+                for (int s = 0; s < kSets; ++s) {
+                    if (EXACT || 16 * VW * s + VW * col < a.dim) {
+                        value_load(x, r, s, reinterpret_cast<const uint16_t*>(vp + (value_lane + r * value_step + 32 * VW * s)));
                     } else {
-                        const u32x2 t = *reinterpret_cast<const u32x2*>(p);
-                        value[r][s][0] = t.x, value[r][s][1] = t.y;
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w)
+                            x.value[r][s][w] = 0;
                     }
                 }
+            x.held = 15;
+        } else {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                x.key[s] = u32x4{0, 0, 0, 0};
+                if (key_at >= 0 && 32 * s + 8 * quarter < a.dim)
+                    x.key[s] = *reinterpret_cast<const u32x4*>(k0 + key_at + 32 * s + 8 * quarter);
             }
+            x.held = 0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int lo = __shfl((int)(unsigned)key_at, 4 * quarter + r), hi = __shfl((int)(key_at >> 32), 4 * quarter + r);
+                const int64_t at = (int64_t)((uint64_t)(unsigned)hi << 32 | (unsigned)lo);
+                x.held |= (unsigned)(at >= 0) << r;
+#pragma unroll
+                for (int s = 0; s < kSets; ++s) {
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w)
+                        x.value[r][s][w] = 0;
+                    if (at >= 0 && 16 * VW * s + VW * col < a.dim)
+                        value_load(x, r, s, v0 + at + 16 * VW * s + VW * col);
+                }
+            }
+        }
+    };
+
+    auto use = [&](Tile& x, int t) {
+        const int j0 = slot_of(t);
+        if (WHOLE) {
+            x.held = (unsigned)__builtin_amdgcn_readfirstlane((int)x.held);
+            if (x.held != 0 && j0 + 16 > end) {
+                // the last tile: slots past the end may hold anything
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (j0 + 4 * quarter + r >= end) {
+                        x.held &= ~(1u << r);
+#pragma unroll
+                        for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                            for (int w = 0; w < kWords; ++w)
+                                x.value[r][s][w] = 0;
+                    }
+            }
+        }
+        float* logits = nullptr;
+        if (a.logits != nullptr)
+            logits = a.logits + ((int64_t)b * a.q_heads + head0 + col) * a.logits_stride + j0 + 4 * quarter;
+        if (!__any(x.held != 0)) {   // holes
+            if (logits != nullptr && col < nheads)
+                *reinterpret_cast<f32x4*>(logits) = f32x4{-kInf, -kInf, -kInf, -kInf};
+            return;
         }
         f32x4 dot = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-            dot = mfma_dot<DT>(key[s], query[s], dot);
-        float x[4], top = -kInf;
+            dot = mfma_dot<DT>(x.key[s], query[s], dot);
+        f32x4 p;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            x[r] = held[r] ? dot[r] * a.scale : -kInf;
-            top = fmaxf(top, x[r]);
-        }
-        if (a.logits != nullptr && col < nheads) {
-            float* to = a.logits + ((int64_t)b * a.q_heads + head0 + col) * a.at.limit + j0 + 4 * quarter;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (j0 + 4 * quarter + r < end)
-                    to[r] = x[r];
-        }
+        for (int r = 0; r < 4; ++r)
+            p[r] = x.held >> r & 1 ? dot[r] * a.scale : -kInf;
+        if (logits != nullptr && col < nheads)
+            *reinterpret_cast<f32x4*>(logits) = p;
+        float top = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
         if (__any(top > m + kSlack)) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
@@ -245,13 +349,32 @@ attention_kernel(Attention a)
         const float ref = m == -kInf ? 0.0f : m;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float p = exp2_hw(x[r] - ref);
-            sum += p;
+            p[r] = exp2_hw(p[r] - ref);
+            sum += p[r];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int s = 0; s < kSets; ++s)
 #pragma unroll
                 for (int e = 0; e < VW; ++e)
-                    acc[s][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, element<DT>(value[r][s], e), acc[s][e], 0, 0, 0);
+                    acc[s][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[r], element<DT>(x.value[r][s], e), acc[s][e], 0, 0, 0);
+    };
+
+    if (tiles > 0) {
+        Tile even, odd;
+        look_up(0);
+        load(even, 0);
+        look_up(1);
+        for (int t = 0; t < tiles; t += 2) {
+            load(odd, t + 1);
+            look_up(t + 2);
+            use(even, t);
+            if (t + 1 >= tiles)
+                break;
+            load(even, t + 2);
+            look_up(t + 3);
+            use(odd, t + 1);
         }
     }
 
@@ -263,15 +386,18 @@ attention_kernel(Attention a)
         red_s[wave][col] = sum;
     }
 #pragma unroll
-    for (int s = 0; s < kSets; ++s)
+    for (int r = 0; r < 4; ++r)
+        if (4 * quarter + r < nheads)
 #pragma unroll
-        for (int e = 0; e < VW; ++e)
+            for (int s = 0; s < kSets; ++s)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                red_o[wave][4 * quarter + r][16 * VW * s + VW * col + e] = acc[s][e][r];
+                for (int e = 0; e < VW; ++e)
+                    red_o[wave][4 * quarter + r][16 * VW * s + VW * col + e] = acc[s][e][r];
     __syncthreads();
-    for (int i = threadIdx.x; i < nheads * a.dim; i += kWaves * 64) {
-        const int h = i / a.dim, d = i % a.dim;
+    for (int i = threadIdx.x; i < nheads * DP; i += kWaves * 64) {
+        const int h = i / DP, d = i % DP;
+        if (!EXACT && d >= a.dim)
+            continue;
         float top = -kInf;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
@@ -279,7 +405,7 @@ attention_kernel(Attention a)
         float o = 0.0f, total = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            const float f = red_m[w][h] == -kInf ? (red_s[w][h] == 0.0f ? 0.0f : 1.0f) : exp2_hw(red_m[w][h] - top);
+            const float f = part_factor(red_m[w][h], red_s[w][h], top);
             o += f * red_o[w][h][d];
             total += f * red_s[w][h];
         }
@@ -296,67 +422,90 @@ attention_kernel(Attention a)
 }
 
 // The maximum and the sum of powers of a query head over the parts that its
-// length reaches.  An empty part has maximum -inf and sum 0.
+// length reaches, by one wave; the same in every lane.  Lane l takes parts l,
+// l + 64, ..., and the lanes' sums meet in a fixed order.
 struct Whole {
     float top, total;
 };
 
-__device__ __forceinline__ float part_factor(float m, float s, float top)
-{
-    return m == -kInf ? (s == 0.0f ? 0.0f : 1.0f) : exp2_hw(m - top);
-}
-
-__device__ __forceinline__ Whole whole(const float* ms, int parts)
+__device__ __forceinline__ Whole whole(const float* ms, int parts, int lane)
 {
     Whole w = {-kInf, 0.0f};
-    for (int p = 0; p < parts; ++p)
+    for (int p = lane; p < parts; p += 64)
         w.top = fmaxf(w.top, ms[2 * p]);
-    for (int p = 0; p < parts; ++p)
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        w.top = fmaxf(w.top, __shfl_xor(w.top, d));
+    for (int p = lane; p < parts; p += 64)
         w.total += part_factor(ms[2 * p], ms[2 * p + 1], w.top) * ms[2 * p + 1];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        w.total += __shfl_xor(w.total, d);
     return w;
 }
 
-// Joins the parts of one query head, in order.
-template <int DT>
-__global__ void __launch_bounds__(128)
-join_kernel(Attention a)
-{
-    const int64_t row = blockIdx.x;
-    const int b = (int)(row / a.q_heads);
-    const int parts = (a.at.length(b) + a.chunk - 1) / a.chunk;
-    const float* ms = a.part_ms + row * a.parts * 2;
-    const Whole w = whole(ms, parts);
-    for (int d = threadIdx.x; d < a.dim; d += 128) {
-        float o = 0.0f;
-        for (int p = 0; p < parts; ++p)
-            o += part_factor(ms[2 * p], ms[2 * p + 1], w.top) * a.part_out[(row * a.parts + p) * a.dim + d];
-        narrow_to<DT>(a.out, row * a.dim + d, w.total == 0.0f ? 0.0f : o / w.total);
-    }
-}
+constexpr int kJoinHeads = 64;   // query heads whose sums a workgroup keeps at a time
 
-// weights[b][kv][j] += sum over the group's heads of 2^(logit - maximum) / sum
+// After the parts: the first `rows` workgroups (none where the length is not
+// split) join a query head's parts, in order; the others add 2^(logit -
+// maximum) / sum over the heads of a group to the weights of 1024 slots.
+template <int DT>
 __global__ void __launch_bounds__(256)
-weights_kernel(Attention a, int blocks)
+join_kernel(Attention a, int rows, int blocks)
 {
-    int item = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if ((int)blockIdx.x < rows) {
+        const int64_t row = blockIdx.x;
+        const int b = (int)(row / a.q_heads);
+        const int parts = (a.at.length(b) + a.chunk - 1) / a.chunk;
+        const float* ms = a.part_ms + row * a.parts * 2;
+        const Whole w = whole(ms, parts, lane);
+        for (int d = threadIdx.x; d < a.dim; d += 256) {
+            float o = 0.0f;
+#pragma unroll 8
+            for (int p = 0; p < parts; ++p)
+                o += part_factor(ms[2 * p], ms[2 * p + 1], w.top) * a.part_out[(row * a.parts + p) * a.dim + d];
+            narrow_to<DT>(a.out, row * a.dim + d, w.total == 0.0f ? 0.0f : o / w.total);
+        }
+        return;
+    }
+    __shared__ Whole heads[kJoinHeads];
+    int item = blockIdx.x - rows;
     const int block = item % blocks;
     item /= blocks;
     const int kv = item % a.heads;
     const int b = item / a.heads;
     const int len = a.at.length(b);
-    const int64_t j = (int64_t)block * 256 + threadIdx.x;
-    if (j >= len)
+    if (block * 1024 >= len)
         return;
     const int parts = (len + a.chunk - 1) / a.chunk;
-    float total = 0.0f;
-    for (int g = 0; g < a.group; ++g) {
-        const int64_t row = (int64_t)b * a.q_heads + kv * a.group + g;
-        const Whole w = whole(a.part_ms + row * a.parts * 2, parts);
-        const float x = a.logits[row * a.at.limit + j];
-        if (w.total != 0.0f)
-            total += exp2_hw(x - (w.top == -kInf ? 0.0f : w.top)) / w.total;
+    const int j = block * 1024 + (int)threadIdx.x * 4;
+    f32x4 total = {0, 0, 0, 0};
+    for (int g0 = 0; g0 < a.group; g0 += kJoinHeads) {
+        const int n = a.group - g0 < kJoinHeads ? a.group - g0 : kJoinHeads;
+        const int64_t row = (int64_t)b * a.q_heads + kv * a.group + g0;
+        __syncthreads();
+        for (int g = wave; g < n; g += 4) {
+            const Whole w = whole(a.part_ms + (row + g) * a.parts * 2, parts, lane);
+            if (lane == 0)
+                heads[g] = Whole{w.top == -kInf ? 0.0f : w.top, w.total == 0.0f ? 0.0f : 1.0f / w.total};
+        }
+        __syncthreads();
+        if (j < len) {
+#pragma unroll 4
+            for (int g = 0; g < n; ++g) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(a.logits + (row + g) * a.logits_stride + j);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    total[r] += exp2_hw(x[r] - heads[g].top) * heads[g].total;
+            }
+        }
     }
-    a.weights[((int64_t)b * a.heads + kv) * a.slots + j] += total;
+    float* to = a.weights + ((int64_t)b * a.heads + kv) * a.slots + j;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (j + r < len)
+            to[r] += total[r];
 }
 
 // ---------------------------------------------------------------- append
