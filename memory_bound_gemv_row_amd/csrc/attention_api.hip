@@ -77,7 +77,7 @@ Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q
     const int64_t items = (int64_t)s->batch * c->heads * p.tiles;
     int64_t chunk = items > 0 ? (int64_t)limit * items / ((int64_t)cus * 4) : limit;
     chunk = (chunk + 63) / 64 * 64;
-    chunk = chunk < 64 ? 64 : (chunk > 1024 ? 1024 : chunk);
+    chunk = chunk < 64 ? 64 : (chunk > kMaxChunk ? kMaxChunk : chunk);
     p.chunk = (int)chunk;
     p.parts = (int)(((int64_t)limit + p.chunk - 1) / p.chunk);
     p.parts = p.parts < 1 ? 1 : p.parts;
@@ -167,7 +167,8 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
     if (p.bytes > 0 && (workspace == nullptr || workspace_bytes < p.bytes || !aligned(workspace, 16)))
         return GEMV_E_INVAL;
     const int64_t items = (int64_t)batch->batch * cache->heads;
-    const int64_t grid = items * p.tiles * p.parts;
+    const int64_t ranges = (int64_t)batch->batch * p.parts;
+    const int64_t grid = cache->heads * (p.tiles > 1 ? (ranges + 7) / 8 * 8 * p.tiles : ranges);
     const int64_t joins = p.parts > 1 ? (int64_t)batch->batch * q_heads : 0;
     int blocks = weights != nullptr ? (int)(((int64_t)a.at.limit + 1023) / 1024) : 0;
     if (!fits(grid, kWaves * 64) || !fits(joins + items * blocks, 256))
@@ -177,6 +178,7 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
     a.v = static_cast<const uint16_t*>(cache->v);
     a.q = static_cast<const uint16_t*>(q);
     a.q_stride = q_stride;
+    a.batch = batch->batch;
     a.q_heads = q_heads;
     a.heads = cache->heads;
     a.dim = cache->head_dim;
@@ -192,6 +194,7 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
     a.logits_stride = p.logits_stride;
     a.weights = weights;
     a.slots = slots;
+    a.weights_wide = slots % 4 == 0 && aligned(weights, 16);
     void* args[] = {(void*)&a};
     if (int rc = launch(attention_for(cache), grid, kWaves * 64, args, stream); rc != GEMV_OK)
         return rc;

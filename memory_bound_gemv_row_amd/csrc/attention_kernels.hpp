@@ -92,11 +92,11 @@ struct Attention {
     const uint16_t* v;
     const uint16_t* q;
     int64_t q_stride;
-    int q_heads, heads, dim;
+    int batch, q_heads, heads, dim;
     int group;        // query heads per key-value head
     int tiles;        // workgroups per key-value head: ceil(group / 16)
     int parts;        // workgroups over the length
-    int chunk;        // slots each takes, a multiple of 16
+    int chunk;        // slots each takes, a multiple of 64
     float scale;      // of the logits, log2(e) included: softmax in powers of two
     void* out;
     float* part_out;  // [batch][q_heads][parts][dim], not divided by the sums
@@ -105,6 +105,7 @@ struct Attention {
     int64_t logits_stride;   // the longest length in whole tiles
     float* weights;   // [batch][heads][slots], or null
     int64_t slots;
+    bool weights_wide;       // rows of weights are 16-byte aligned
 };
 
 // What brings a part's sums to the common maximum `top`.  An empty part has
@@ -115,14 +116,19 @@ __device__ __forceinline__ float part_factor(float m, float s, float top)
 }
 
 constexpr int kWaves = 4;
+constexpr int kMaxChunk = 1024;  // slots of a part: 16 tiles a wave
 constexpr float kSlack = 8.0f;   // powers of two that a logit may pass the reference maximum by
 
-__device__ __forceinline__ const uint16_t* uniform(const uint16_t* p)
+// Loads through a buffer descriptor: an address outside it gives zeros and
+// reads nothing, so a lane without an element, a slot past the end and a hole
+// need no branch.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr int kOnce = 2;                     // cache policy: read once, not to be kept
+constexpr unsigned kNowhere = 0x80000000u;   // past every descriptor's end
+
+__device__ __forceinline__ Buffer buffer(const uint16_t* p, unsigned bytes)
 {
-    const uint64_t u = reinterpret_cast<uint64_t>(p);
-    const unsigned lo = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)u);
-    const unsigned hi = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(u >> 32));
-    return reinterpret_cast<const uint16_t*>((uint64_t)hi << 32 | lo);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, (int)bytes, 0x00027000);
 }
 
 // One workgroup: up to 16 query heads of one key-value head of one sequence,
@@ -143,13 +149,11 @@ __device__ __forceinline__ const uint16_t* uniform(const uint16_t* p)
 // with each tile.
 //
 // A wave loads its next tile while it multiplies the current one.  Where
-// pages are whole numbers of tiles (WHOLE), a tile has one page: its address
-// is the same for all lanes, and one load per 64 tiles brings the page
-// numbers.  Otherwise each lane looks its key's slot up a tile ahead, and the
-// addresses of the values come from the lanes that hold those keys.  EXACT:
-// the head's size is DP, so no lane is without an element.
+// pages are whole numbers of tiles (WHOLE), a tile has one page and its
+// address is the same for all lanes; otherwise each row has an address of its
+// own.  EXACT: the head's size is DP, so no lane is without an element.
 template <int DT, int DP, bool WHOLE, bool EXACT>
-__global__ void __launch_bounds__(kWaves * 64)
+__global__ void __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2)
 attention_kernel(Attention a)
 {
     constexpr int kSteps = DP / 32;              // of 32 elements of the dot products
@@ -163,13 +167,26 @@ attention_kernel(Attention a)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, quarter = lane >> 4;
-    int item = blockIdx.x;
-    const int part = item % a.parts;
-    item /= a.parts;
-    const int tile = item % a.tiles;
-    item /= a.tiles;
-    const int kv = item % a.heads;
-    const int b = item / a.heads;
+    // Neighbouring workgroups go to the eight XCDs in turn.  Heads vary
+    // fastest, so the rows of one token, which lie together, are read at about
+    // the same time; each XCD's share moves on by a head from one token range
+    // to the next, so that it sees every head's part of the address space; and
+    // parts vary slowest, so that the ends that only long sequences reach are
+    // spread over all XCDs.
+    // Where a head's queries need several workgroups, those that read the same
+    // keys are a multiple of eight apart: on one XCD, at about the same time.
+    const int turn = (int)blockIdx.x / a.heads;
+    const int kv = ((int)blockIdx.x + turn) % a.heads;
+    int tile = 0, range = turn;
+    if (a.tiles > 1) {
+        const int eight = turn / (8 * a.tiles), rest = turn - eight * 8 * a.tiles;
+        tile = rest >> 3;
+        range = eight * 8 + (rest & 7);
+        if (range >= a.batch * a.parts)
+            return;
+    }
+    const int b = range % a.batch;
+    const int part = range / a.batch;
     const int len = __builtin_amdgcn_readfirstlane(a.at.length(b));
     const int64_t first = (int64_t)part * a.chunk;
     if (part > 0 && first >= len)
@@ -201,34 +218,28 @@ attention_kernel(Attention a)
         unsigned value[4][kSets][kWords];
         unsigned held;   // bit r: slot 4 quarter + r is there
     };
-    const int tiles = (end - begin - wave * 16 + kWaves * 16 - 1) / (kWaves * 16);   // of this wave; <= 0: none
-    auto slot_of = [&](int t) { return begin + (wave + t * kWaves) * 16; };
+    auto slot_of = [&](int t) { return begin + (wave + t * kWaves) * 16; };   // tile t of this wave
     const uint16_t* k0 = a.k + kv * a.at.stride_head;
     const uint16_t* v0 = a.v + kv * a.at.stride_head;
 
-    auto value_load = [&](Tile& x, int r, int s, const uint16_t* p) {
-        if constexpr (VW == 8) {
-            const u32x4 t = *reinterpret_cast<const u32x4*>(p);
-            x.value[r][s][0] = t.x, x.value[r][s][1] = t.y, x.value[r][s][2] = t.z, x.value[r][s][3] = t.w;
-        } else {
-            const u32x2 t = *reinterpret_cast<const u32x2*>(p);
-            x.value[r][s][0] = t.x, x.value[r][s][1] = t.y;
-        }
-    };
-    // WHOLE: the page of tile t of this wave, in lane t % 64; otherwise the
-    // offset of this lane's key of the tile to be loaded next
+    // the pages of this part, looked up once so that no tile's loads wait for
+    // a page number: WHOLE, tile t of this wave in lane t; otherwise every slot's in LDS
     int pages = -1;
-    int64_t key_at = -1;
-    auto look_up = [&](int t) {
-        if constexpr (WHOLE) {
-            if ((t & 63) == 0) {
-                const int64_t j = (int64_t)begin + (wave + (int64_t)(t + lane) * kWaves) * 16;
-                pages = j < end ? a.at.table[b * a.at.table_stride + a.at.page_of.by((int)j)] : -1;
-            }
-        } else {
-            const int64_t j = (int64_t)begin + (wave + (int64_t)t * kWaves) * 16 + col;
-            key_at = j < end ? a.at.offset(b, (int)j) : -1;
-        }
+    __shared__ int32_t slot_page[WHOLE ? 1 : kMaxChunk];
+    if constexpr (WHOLE) {
+        const int64_t j = (int64_t)begin + (wave + lane * kWaves) * 16;
+        if (j < a.at.limit)
+            pages = a.at.table[b * a.at.table_stride + a.at.page_of.by((int)j)];
+    } else {
+        for (int i = threadIdx.x; i < a.chunk; i += kWaves * 64)
+            slot_page[i] = begin + i < end ? a.at.table[b * a.at.table_stride + a.at.page_of.by(begin + i)] : -1;
+        __syncthreads();
+    }
+    auto offset_at = [&](int j) -> int64_t {   // of slot j < end, where !WHOLE
+        const int page = slot_page[j - begin];
+        if ((unsigned)page >= (unsigned)a.at.pages)
+            return -1;
+        return page * a.at.stride_page + (int64_t)(j - a.at.page_of.by(j) * a.at.page_size) * a.at.stride_slot;
     };
     // byte offsets of this lane's pieces from the tile's first slot (WHOLE;
     // the host has checked that 16 slots span less than 2^31 bytes)
@@ -237,37 +248,39 @@ attention_kernel(Attention a)
     const unsigned value_step = (unsigned)a.at.stride_slot * 2;
 
     auto load = [&](Tile& x, int t) {
+        const int j = slot_of(t);
         if constexpr (WHOLE) {
             const int page = __builtin_amdgcn_readlane(pages, t & 63);
+            const bool there = j < end && (unsigned)page < (unsigned)a.at.pages;
+            const int i = there ? j - a.at.page_of.by(j) * a.at.page_size : 0;
+            const int64_t at = there ? page * a.at.stride_page + (int64_t)i * a.at.stride_slot : 0;
+            const Buffer keys = buffer(k0 + at, there ? kNowhere - 1 : 0), values = buffer(v0 + at, there ? kNowhere - 1 : 0);
+            const int left = there ? end - j : 0;   // slots of the tile before the end
+            const unsigned key_off = col < left ? key_lane : kNowhere;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                x.key[s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                    keys, EXACT || 32 * s + 8 * quarter < a.dim ? key_off + 64 * s : kNowhere, 0, 0));
             x.held = 0;
-            if ((unsigned)page >= (unsigned)a.at.pages)
-                return;                         // past the end, or a hole: neither loaded nor used
-            const int j = slot_of(t);
-            const int i = j - a.at.page_of.by(j) * a.at.page_size;
-            const int64_t at = page * a.at.stride_page + (int64_t)i * a.at.stride_slot;
-            const char* kp = reinterpret_cast<const char*>(uniform(k0 + at));
-            const char* vp = reinterpret_cast<const char*>(uniform(v0 + at));
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                if (EXACT || 32 * s + 8 * quarter < a.dim)
-                    x.key[s] = *reinterpret_cast<const u32x4*>(kp + (key_lane + 64 * s));
-                else
-                    x.key[s] = u32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r) {
+                const bool mine = 4 * quarter + r < left;
+                x.held |= (unsigned)mine << r;
+                const unsigned off = mine ? value_lane + r * value_step : kNowhere;
 #pragma unroll
                 for (int s = 0; s < kSets; ++s) {
-                    if (EXACT || 16 * VW * s + VW * col < a.dim) {
-                        value_load(x, r, s, reinterpret_cast<const uint16_t*>(vp + (value_lane + r * value_step + 32 * VW * s)));
+                    const unsigned o = EXACT || 16 * VW * s + VW * col < a.dim ? off + 32 * VW * s : kNowhere;
+                    if constexpr (VW == 8) {
+                        const u32x4 w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(values, o, 0, kOnce));
+                        x.value[r][s][0] = w.x, x.value[r][s][1] = w.y, x.value[r][s][2] = w.z, x.value[r][s][3] = w.w;
                     } else {
-#pragma unroll
-                        for (int w = 0; w < kWords; ++w)
-                            x.value[r][s][w] = 0;
+                        const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(values, o, 0, kOnce));
+                        x.value[r][s][0] = w.x, x.value[r][s][1] = w.y;
                     }
                 }
-            x.held = 15;
+            }
         } else {
+            const int64_t key_at = j + col < end ? offset_at(j + col) : -1;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 x.key[s] = u32x4{0, 0, 0, 0};
@@ -277,16 +290,23 @@ attention_kernel(Attention a)
             x.held = 0;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int lo = __shfl((int)(unsigned)key_at, 4 * quarter + r), hi = __shfl((int)(key_at >> 32), 4 * quarter + r);
-                const int64_t at = (int64_t)((uint64_t)(unsigned)hi << 32 | (unsigned)lo);
+                const int64_t at = j + 4 * quarter + r < end ? offset_at(j + 4 * quarter + r) : -1;
                 x.held |= (unsigned)(at >= 0) << r;
 #pragma unroll
                 for (int s = 0; s < kSets; ++s) {
 #pragma unroll
                     for (int w = 0; w < kWords; ++w)
                         x.value[r][s][w] = 0;
-                    if (at >= 0 && 16 * VW * s + VW * col < a.dim)
-                        value_load(x, r, s, v0 + at + 16 * VW * s + VW * col);
+                    if (at >= 0 && 16 * VW * s + VW * col < a.dim) {
+                        const uint16_t* p = v0 + at + 16 * VW * s + VW * col;
+                        if constexpr (VW == 8) {
+                            const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+                            x.value[r][s][0] = w.x, x.value[r][s][1] = w.y, x.value[r][s][2] = w.z, x.value[r][s][3] = w.w;
+                        } else {
+                            const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+                            x.value[r][s][0] = w.x, x.value[r][s][1] = w.y;
+                        }
+                    }
                 }
             }
         }
@@ -294,30 +314,9 @@ attention_kernel(Attention a)
 
     auto use = [&](Tile& x, int t) {
         const int j0 = slot_of(t);
-        if (WHOLE) {
-            x.held = (unsigned)__builtin_amdgcn_readfirstlane((int)x.held);
-            if (x.held != 0 && j0 + 16 > end) {
-                // the last tile: slots past the end may hold anything
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (j0 + 4 * quarter + r >= end) {
-                        x.held &= ~(1u << r);
-#pragma unroll
-                        for (int s = 0; s < kSets; ++s)
-#pragma unroll
-                            for (int w = 0; w < kWords; ++w)
-                                x.value[r][s][w] = 0;
-                    }
-            }
-        }
         float* logits = nullptr;
         if (a.logits != nullptr)
             logits = a.logits + ((int64_t)b * a.q_heads + head0 + col) * a.logits_stride + j0 + 4 * quarter;
-        if (!__any(x.held != 0)) {   // holes
-            if (logits != nullptr && col < nheads)
-                *reinterpret_cast<f32x4*>(logits) = f32x4{-kInf, -kInf, -kInf, -kInf};
-            return;
-        }
         f32x4 dot = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
@@ -326,7 +325,7 @@ attention_kernel(Attention a)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             p[r] = x.held >> r & 1 ? dot[r] * a.scale : -kInf;
-        if (logits != nullptr && col < nheads)
+        if (logits != nullptr && col < nheads && j0 < end)
             *reinterpret_cast<f32x4*>(logits) = p;
         float top = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
         if (__any(top > m + kSlack)) {
@@ -361,21 +360,14 @@ attention_kernel(Attention a)
                     acc[s][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[r], element<DT>(x.value[r][s], e), acc[s][e], 0, 0, 0);
     };
 
-    if (tiles > 0) {
-        Tile even, odd;
-        look_up(0);
-        load(even, 0);
-        look_up(1);
-        for (int t = 0; t < tiles; t += 2) {
-            load(odd, t + 1);
-            look_up(t + 2);
-            use(even, t);
-            if (t + 1 >= tiles)
-                break;
-            load(even, t + 2);
-            look_up(t + 3);
-            use(odd, t + 1);
-        }
+    // in pairs: a tile past the last has nothing held and adds nothing
+    Tile even, odd;
+    load(even, 0);
+    for (int t = 0; slot_of(t) < end; t += 2) {
+        load(odd, t + 1);
+        use(even, t);
+        load(even, t + 2);
+        use(odd, t + 1);
     }
 
     // the waves' parts meet in LDS
@@ -502,10 +494,14 @@ join_kernel(Attention a, int rows, int blocks)
         }
     }
     float* to = a.weights + ((int64_t)b * a.heads + kv) * a.slots + j;
+    if (a.weights_wide && j + 4 <= len) {
+        *reinterpret_cast<f32x4*>(to) += total;
+    } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (j + r < len)
-            to[r] += total[r];
+        for (int r = 0; r < 4; ++r)
+            if (j + r < len)
+                to[r] += total[r];
+    }
 }
 
 // ---------------------------------------------------------------- append
