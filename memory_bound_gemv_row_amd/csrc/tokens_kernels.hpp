@@ -266,68 +266,436 @@ __device__ __forceinline__ i32x4 load16(const int8_t* p, int row, int rows, int 
     return v;
 }
 
-// Any size and alignment.  A workgroup of four waves owns 64 tokens by 64
-// outputs, each wave a 32 x 32 quarter of it; 128 columns of both operands
-// go through LDS at a time, loaded into registers while the step before is
-// multiplied.  v_mfma_i32_32x32x32_i8: lane l holds row (column) l % 32 and 16
-// of the 32 summed values; register r of its result is row
-// 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32.  A 16-byte chunk c of row r
-// is kept at c ^ (r / 2 % 8), so that the 16 rows that one read phase takes
-// lie in 16 different 16-byte columns of LDS.
-template <int DT>
-__global__ void __launch_bounds__(256)
-gemm_q8_any(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale, const int8_t* __restrict__ x,
-            const float* __restrict__ x_scale, void* __restrict__ y, int T, int M, int N, int tiles_m)
+// ---------------------------------------------------------------- product, large
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr unsigned kNowhere = 0xFFFFFF00u;   // past every descriptor's end: such loads give zeros
+
+__device__ __forceinline__ Buffer rows_buffer(const int8_t* p, int row, int rows, int tile, int N)
 {
-    __shared__ i32x4 lx[64 * 8];
-    __shared__ i32x4 la[64 * 8];
+    const int64_t n = rows - row < tile ? rows - row : tile;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p) + (int64_t)row * N, 0, (int)(n > 0 ? n * N : 0),
+                                             0x00027000);
+}
+
+// Sixteen bytes of each lane, from its offset in the descriptor to its place
+// behind `to` (the same address for all lanes): straight to LDS.
+__device__ __forceinline__ void load_to_lds([[maybe_unused]] Buffer from, [[maybe_unused]] unsigned offset,
+                                            [[maybe_unused]] i32x4* to)
+{
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass does not know this size
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, offset, 0, 0, 0);
+#endif
+}
+
+// Workgroups k, k + 8, ... run on XCD k: the tile of workgroup i of n, such
+// that each XCD takes a run of neighbouring ones.
+__device__ __forceinline__ int tile_of(int i, int n)
+{
+    const int xcd = i & 7, share = n >> 3, more = n & 7;
+    return xcd * share + (xcd < more ? xcd : more) + (i >> 3);
+}
+
+// One tile of BT tokens by BM outputs, from t0 and m0, by TW x MW waves, each
+// a BT / TW by BM / MW part of it in 32 x 32 products.  128 columns of both
+// operands at a time go straight from memory to LDS, 16 bytes a lane, into one
+// of two buffers while the other is multiplied.  The memory pipe writes a
+// wave's 64 pieces one after the other, so the pieces are put in their
+// swizzled order (piece c of row r at c ^ (r / 2 % 8)) by choosing which piece a
+// lane reads; rows past the end and columns past N read as zeros.
+template <int DT, int BT, int BM, int TW, int MW>
+__device__ __forceinline__ void
+gemm_tile(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale, const int8_t* __restrict__ x,
+          const float* __restrict__ x_scale, void* __restrict__ y, int T, int M, int N, int t0, int m0,
+          i32x4* even_x, i32x4* even_a, i32x4* odd_x, i32x4* odd_a)
+{
+    constexpr int kThreads = TW * MW * 64;
+    constexpr int FT = BT / TW / 32, FM = BM / MW / 32;   // products of a wave
+    constexpr int LX = BT * 8 / kThreads, LA = BM * 8 / kThreads;
+    static_assert(LX > 0 && LA > 0 && FT > 0 && FM > 0, "every wave loads and multiplies");
+    static_assert(kThreads / 8 % 16 == 0, "the swizzle repeats over the rounds of loads");
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
-    const int t0 = (int)(blockIdx.x / tiles_m) * 64;
-    const int m0 = (int)(blockIdx.x % tiles_m) * 64;
-    const int wt = (wave >> 1) * 32, wm = (wave & 1) * 32;
-    i32x16 acc = {};
-    i32x4 vx[2], va[2];
-    auto fetch = [&](int k0) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Buffer from_x = rows_buffer(x, t0, T, BT, N), from_a = rows_buffer(A, m0, M, BM, N);
+    // piece s = i * kThreads + thread of a buffer: row s / 8, place s % 8
+    unsigned off_x[LX], off_a[LA];
+    const int row = threadIdx.x >> 3, piece = (threadIdx.x & 7) ^ ((row >> 1) & 7);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int s = (int)threadIdx.x + 256 * i;
-            const int col = k0 + (s & 7) * 16;
-            vx[i] = col < N ? load16(x, t0 + (s >> 3), T, col, N) : i32x4{0, 0, 0, 0};
-            va[i] = col < N ? load16(A, m0 + (s >> 3), M, col, N) : i32x4{0, 0, 0, 0};
+    for (int i = 0; i < LX; ++i)
+        off_x[i] = (unsigned)((row + i * (kThreads / 8)) * N + piece * 16);
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+        off_a[i] = (unsigned)((row + i * (kThreads / 8)) * N + piece * 16);
+
+    auto fetch = [&](i32x4* to_x, i32x4* to_a, int k0) {
+        const bool in = k0 + piece * 16 < N;
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            load_to_lds(from_x, in ? off_x[i] + k0 : kNowhere, to_x + i * kThreads + wave * 64);
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            load_to_lds(from_a, in ? off_a[i] + k0 : kNowhere, to_a + i * kThreads + wave * 64);
+    };
+
+    i32x16 acc[FT][FM];
+#pragma unroll
+    for (int i = 0; i < FT; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            acc[i][j] = i32x16{};
+    const int rx = (wave / MW) * (BT / TW) + (lane & 31), ra = (wave % MW) * (BM / MW) + (lane & 31);
+    const int swizzle = ((lane & 31) >> 1) & 7;   // the same for every product: rows differ by multiples of 32
+
+    // One step of 32 columns: its pieces are read while the step before is
+    // multiplied.
+    struct Step {
+        i32x4 x[FT], a[FM];
+    };
+    auto read = [&](Step& f, const i32x4* lx, const i32x4* la, int k) {
+        const int c = (2 * k + (lane >> 5)) ^ swizzle;
+#pragma unroll
+        for (int i = 0; i < FT; ++i)
+            f.x[i] = lx[(rx + 32 * i) * 8 + c];
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            f.a[j] = la[(ra + 32 * j) * 8 + c];
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](const Step& f) {
+#pragma unroll
+        for (int i = 0; i < FT; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.x[i], f.a[j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // All of this wave's reads of the current buffer are in registers and its
+    // pieces of the next one in LDS; after the barrier every wave's are.
+    auto turn = [&] {
+        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) and lgkmcnt(0)
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    Step f, g;
+    auto stage = [&](const i32x4* lx, const i32x4* la, i32x4* next_x, i32x4* next_a, int k0) {
+        fetch(next_x, next_a, k0);
+        __builtin_amdgcn_sched_barrier(0);
+        read(g, lx, la, 1);
+        multiply(f);
+        read(f, lx, la, 2);
+        multiply(g);
+        read(g, lx, la, 3);
+        multiply(f);
+        turn();
+        read(f, next_x, next_a, 0);
+        multiply(g);
+    };
+    fetch(even_x, even_a, 0);
+    turn();
+    read(f, even_x, even_a, 0);
+    for (int k0 = 0; k0 < N; k0 += 256) {
+        stage(even_x, even_a, odd_x, odd_a, k0 + 128);
+        stage(odd_x, odd_a, even_x, even_a, k0 + 256);
+    }
+
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int m = m0 + ra + 32 * j;
+        if (m >= M)
+            continue;
+        const float s = half_value(scale[m]);
+#pragma unroll
+        for (int i = 0; i < FT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int t = t0 + (wave / MW) * (BT / TW) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                if (t < T)
+                    store<DT>(y, (int64_t)t * M + m, acc[i][j][r], x_scale[t], s);
+            }
+    }
+}
+
+// Preconditions (host): N % 16 == 0, N >= 16, A and x 16-byte aligned.
+//
+// Tiles of 256 x 256, one to a CU, by 16 waves of 64 x 64 (8 waves of 128 x 64
+// read a quarter less LDS but were slower: 8192 x 8192 x 8192 in 507 against
+// 482 us).  The first `whole` tiles are done so; the rest, where they are too
+// few to fill the CUs once more, in halves of 128 outputs.  Each XCD takes its
+// run of tiles in bands of four rows of tiles, so that what it has in flight
+// at a time reads few different rows of either operand.
+template <int DT>
+__global__ void __launch_bounds__(1024)
+gemm_q8_tiles(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale, const int8_t* __restrict__ x,
+              const float* __restrict__ x_scale, void* __restrict__ y, int T, int M, int N, int tiles_t, int tiles_m,
+              int whole)
+{
+    __shared__ i32x4 even_x[256 * 8];
+    __shared__ i32x4 even_a[256 * 8];
+    __shared__ i32x4 odd_x[256 * 8];
+    __shared__ i32x4 odd_a[256 * 8];
+    const int i = blockIdx.x;
+    const bool half = i >= whole;
+    const int rest = half ? tile_of(i - whole, 2 * (tiles_t * tiles_m - whole)) : 0;
+    const int at = half ? whole + (rest >> 1) : tile_of(i, whole);
+    const int band = at / (4 * tiles_m), in_band = at - band * 4 * tiles_m;
+    const int band_rows = tiles_t - band * 4 < 4 ? tiles_t - band * 4 : 4;
+    const int t0 = (band * 4 + in_band % band_rows) * 256, m0 = in_band / band_rows * 256;
+    if (!half)
+        gemm_tile<DT, 256, 256, 4, 4>(A, scale, x, x_scale, y, T, M, N, t0, m0, even_x, even_a, odd_x, odd_a);
+    else if (m0 + (rest & 1) * 128 < M)
+        gemm_tile<DT, 256, 128, 4, 4>(A, scale, x, x_scale, y, T, M, N, t0, m0 + (rest & 1) * 128, even_x, even_a, odd_x,
+                                      odd_a);
+}
+
+// ---------------------------------------------------------------- product, few tokens
+// Waits until this wave's reads of LDS are in registers and all but its LEFT
+// newest loads have come, then for the workgroup's other waves.  A barrier of
+// its own kind: __syncthreads() would wait for every load.
+template <int LEFT>
+__device__ __forceinline__ void wait_and_meet()
+{
+    static_assert(LEFT >= 0 && LEFT < 64, "the counter has six bits");
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((LEFT & 15) | (LEFT >> 4) << 14 | 0x0070);   // vmcnt, lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Stores a tile's products, register r of acc[i][j] being token
+// 4 (l / 16) + r and output l % 16 of its 16 x 16.  Where the waves along WK
+// hold parts of the sums, they first meet in `sums` by integer atomics, whose
+// order does not matter; no wave may still need that part of LDS.
+template <int DT, int BT, int BM, int WT, int WM, int WK>
+__device__ __forceinline__ void
+store_tile(const i32x4 (&acc)[BT / WT / 16][BM / WM / 16], [[maybe_unused]] int* sums, const uint16_t* __restrict__ scale,
+           const float* __restrict__ x_scale, void* __restrict__ y, int T, int M, int t0, int m0)
+{
+    constexpr int kThreads = WT * WM * WK * 64;
+    constexpr int FT = BT / WT / 16, FM = BM / WM / 16;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, low = lane & 15;
+    const int wm = wave / WK % WM, wt = wave / WK / WM;
+    if constexpr (WK == 1) {
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int m = m0 + (wm * FM + j) * 16 + low;
+            if (m >= M)
+                continue;
+            const float s = half_value(scale[m]);
+#pragma unroll
+            for (int i = 0; i < FT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = t0 + (wt * FT + i) * 16 + 4 * (lane >> 4) + r;
+                    if (t < T)
+                        store<DT>(y, (int64_t)t * M + m, acc[i][j][r], x_scale[t], s);
+                }
+        }
+    } else {
+        wait_and_meet<0>();
+        for (int i = threadIdx.x; i < BT * BM; i += kThreads)
+            sums[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < FT; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    atomicAdd(&sums[((wt * FT + i) * 16 + 4 * (lane >> 4) + r) * BM + (wm * FM + j) * 16 + low],
+                              acc[i][j][r]);
+        __syncthreads();
+        for (int i = threadIdx.x; i < BT * BM; i += kThreads) {
+            const int t = t0 + i / BM, m = m0 + i % BM;
+            if (t < T && m < M)
+                store<DT>(y, (int64_t)t * M + m, sums[i], x_scale[t], half_value(scale[m]));
+        }
+    }
+}
+
+// Preconditions (host): N % 16 == 0, N >= 16, A and x 16-byte aligned.
+//
+// For products whose time is that of reading A: a workgroup of WT x WM x WK
+// waves owns BT tokens by BM outputs, chosen so that the outputs fill the card,
+// and keeps S - 1 stages of C columns of both operands on their way to LDS,
+// whose S buffers it goes round.  Waves along WK take every WK-th step of 64
+// columns.  v_mfma_i32_16x16x64_i8: lane l holds row (column) l % 16
+// and columns 16 (l / 16) .. + 15 of the 64 summed; register r of its result
+// is row 4 (l / 16) + r, column l % 16.
+template <int DT, int BT, int BM, int WT, int WM, int WK, int C, int S>
+__global__ void __launch_bounds__(WT * WM * WK * 64)
+gemm_q8_stream(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale, const int8_t* __restrict__ x,
+               const float* __restrict__ x_scale, void* __restrict__ y, int T, int M, int N, int tiles_t)
+{
+    constexpr int kThreads = WT * WM * WK * 64;
+    constexpr int FT = BT / WT / 16, FM = BM / WM / 16;
+    constexpr int kRow = C / 16;                          // pieces of a row
+    constexpr int kPieces = (BT + BM) * kRow, L = kPieces / kThreads;
+    static_assert(kPieces % kThreads == 0 && kThreads % kRow == 0 && S <= 8, "whole rounds of loads");
+    static_assert((kThreads / kRow) % 16 == 0, "the swizzle repeats over the rounds of loads");
+    static_assert(BT % (kThreads / kRow) == 0, "a round loads rows of one operand");
+    static_assert(WK == 1 || BT * BM * 4 <= kPieces * 16, "the sums fit one buffer");
+    constexpr int kSteps = C / 64 / WK;
+    // a buffer each, so that the compiler knows which of them a load fills
+    __shared__ i32x4 b0[kPieces];
+    __shared__ i32x4 b1[kPieces];
+    __shared__ i32x4 b2[S > 2 ? kPieces : 1];
+    __shared__ i32x4 b3[S > 3 ? kPieces : 1];
+    __shared__ i32x4 b4[S > 4 ? kPieces : 1];
+    __shared__ i32x4 b5[S > 5 ? kPieces : 1];
+    __shared__ i32x4 b6[S > 6 ? kPieces : 1];
+    __shared__ i32x4 b7[S > 7 ? kPieces : 1];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wk = wave % WK, wm = wave / WK % WM, wt = wave / WK / WM;
+    const int at = tile_of(blockIdx.x, gridDim.x);
+    const int t0 = at % tiles_t * BT, m0 = at / tiles_t * BM;
+    const Buffer from_x = rows_buffer(x, t0, T, BT, N), from_a = rows_buffer(A, m0, M, BM, N);
+    auto turned = [](int r) { return kRow >= 16 ? r & 15 : (r >> 1) & 7; };
+    const int row = threadIdx.x / kRow, piece = (threadIdx.x % kRow) ^ turned(row);
+
+    auto fetch = [&](i32x4* to, int k0) {
+        const int k = k0 + piece * 16;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int r = row + i * (kThreads / kRow);
+            const bool of_x = i * (kThreads / kRow) < BT;
+            const unsigned off = k < N ? (unsigned)((of_x ? r : r - BT) * N + k) : kNowhere;
+            load_to_lds(of_x ? from_x : from_a, off, to + i * kThreads + wave * 64);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    i32x4 acc[FT][FM];
+#pragma unroll
+    for (int i = 0; i < FT; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            acc[i][j] = i32x4{0, 0, 0, 0};
+    const int low = lane & 15;
+    auto multiply = [&](const i32x4* b) {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const int c = (4 * (k * WK + wk) + (lane >> 4)) ^ turned(low);
+            i32x4 vx[FT], va[FM];
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+                va[j] = b[(BT + (wm * FM + j) * 16 + low) * kRow + c];
+#pragma unroll
+            for (int i = 0; i < FT; ++i)
+                vx[i] = b[((wt * FT + i) * 16 + low) * kRow + c];
+#pragma unroll
+            for (int i = 0; i < FT; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vx[i], va[j], acc[i][j], 0, 0, 0);
         }
     };
-    fetch(0);
-    for (int k0 = 0; k0 < N; k0 += 128) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int s = (int)threadIdx.x + 256 * i;
-            const int r = s >> 3, c = s & 7;
-            lx[r * 8 + (c ^ ((r >> 1) & 7))] = vx[i];
-            la[r * 8 + (c ^ ((r >> 1) & 7))] = va[i];
-        }
-        __syncthreads();
-        if (k0 + 128 < N)
-            fetch(k0 + 128);
-        const int rx = wt + (lane & 31), ra = wm + (lane & 31);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int c = 2 * k + (lane >> 5);
-            acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(lx[rx * 8 + (c ^ ((rx >> 1) & 7))],
-                                                        la[ra * 8 + (c ^ ((ra >> 1) & 7))], acc, 0, 0, 0);
-        }
+    // this wave's pieces of the stage have come, then every wave's, and every
+    // wave is done with the buffer that is filled next
+    auto stage = [&](const i32x4* now, i32x4* next, int k0) {
+        wait_and_meet<L * (S - 2)>();
+        fetch(next, k0 + (S - 1) * C);
+        multiply(now);
+    };
+    fetch(b0, 0);
+    if constexpr (S > 2) fetch(b1, C);
+    if constexpr (S > 3) fetch(b2, 2 * C);
+    if constexpr (S > 4) fetch(b3, 3 * C);
+    if constexpr (S > 5) fetch(b4, 4 * C);
+    if constexpr (S > 6) fetch(b5, 5 * C);
+    if constexpr (S > 7) fetch(b6, 6 * C);
+    i32x4* const last = S == 2 ? b1 : S == 3 ? b2 : S == 4 ? b3 : S == 5 ? b4 : S == 6 ? b5 : S == 7 ? b6 : b7;
+    for (int k0 = 0; k0 < N; k0 += S * C) {
+        stage(b0, last, k0);
+        if (k0 + C >= N) break;
+        stage(b1, b0, k0 + C);
+        if constexpr (S > 2) { if (k0 + 2 * C >= N) break; stage(b2, b1, k0 + 2 * C); }
+        if constexpr (S > 3) { if (k0 + 3 * C >= N) break; stage(b3, b2, k0 + 3 * C); }
+        if constexpr (S > 4) { if (k0 + 4 * C >= N) break; stage(b4, b3, k0 + 4 * C); }
+        if constexpr (S > 5) { if (k0 + 5 * C >= N) break; stage(b5, b4, k0 + 5 * C); }
+        if constexpr (S > 6) { if (k0 + 6 * C >= N) break; stage(b6, b5, k0 + 6 * C); }
+        if constexpr (S > 7) { if (k0 + 7 * C >= N) break; stage(b7, b6, k0 + 7 * C); }
     }
-    const int m = m0 + wm + (lane & 31);
-    if (m >= M)
-        return;
-    const float s = half_value(scale[m]);
+    store_tile<DT, BT, BM, WT, WM, WK>(acc, reinterpret_cast<int*>(b0), scale, x_scale, y, T, M, t0, m0);
+}
+
+// Any size and alignment.  The same tiles, but rows of any alignment come
+// through registers, two stages of C columns ahead, and are written to one of
+// two buffers; columns past N are zeros there.
+template <int DT, int BT, int BM, int WT, int WM, int WK, int C>
+__global__ void __launch_bounds__(WT * WM * WK * 64)
+gemm_q8_any(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale, const int8_t* __restrict__ x,
+            const float* __restrict__ x_scale, void* __restrict__ y, int T, int M, int N, int tiles_t)
+{
+    constexpr int kThreads = WT * WM * WK * 64;
+    constexpr int FT = BT / WT / 16, FM = BM / WM / 16;
+    constexpr int kRow = C / 16;
+    constexpr int kPieces = (BT + BM) * kRow, L = kPieces / kThreads;
+    static_assert(kPieces % kThreads == 0 && BT * kRow % kThreads == 0, "whole rounds of loads, each of one operand");
+    static_assert(WK == 1 || BT * BM * 4 <= kPieces * 16, "the sums fit one buffer");
+    constexpr int kSteps = C / 64 / WK;
+    __shared__ i32x4 buffers[2][kPieces];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wk = wave % WK, wm = wave / WK % WM, wt = wave / WK / WM;
+    const int at = tile_of(blockIdx.x, gridDim.x);
+    const int t0 = at % tiles_t * BT, m0 = at / tiles_t * BM;
+    auto turned = [](int r) { return kRow >= 16 ? r & 15 : (r >> 1) & 7; };
+
+    struct Stage {
+        i32x4 v[L];
+    };
+    auto fetch = [&](Stage& s, int k0) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int t = t0 + wt + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        if (t < T)
-            store<DT>(y, (int64_t)t * M + m, acc[r], x_scale[t], s);
+        for (int i = 0; i < L; ++i) {
+            const int piece = i * kThreads + (int)threadIdx.x, r = piece / kRow, col = k0 + piece % kRow * 16;
+            const bool of_x = i * kThreads < BT * kRow;
+            s.v[i] = i32x4{0, 0, 0, 0};
+            if (col < N)
+                s.v[i] = of_x ? load16(x, t0 + r, T, col, N) : load16(A, m0 + r - BT, M, col, N);
+        }
+    };
+    i32x4 acc[FT][FM];
+#pragma unroll
+    for (int i = 0; i < FT; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            acc[i][j] = i32x4{0, 0, 0, 0};
+    const int low = lane & 15;
+    auto stage = [&](Stage& s, i32x4* b, int k0) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int piece = i * kThreads + (int)threadIdx.x, r = piece / kRow;
+            b[r * kRow + ((piece % kRow) ^ turned(r))] = s.v[i];
+        }
+        __syncthreads();   // the other buffer was read before the barrier before this
+        fetch(s, k0 + 2 * C);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const int c = (4 * (k * WK + wk) + (lane >> 4)) ^ turned(low);
+            i32x4 vx[FT], va[FM];
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+                va[j] = b[(BT + (wm * FM + j) * 16 + low) * kRow + c];
+#pragma unroll
+            for (int i = 0; i < FT; ++i)
+                vx[i] = b[((wt * FT + i) * 16 + low) * kRow + c];
+#pragma unroll
+            for (int i = 0; i < FT; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vx[i], va[j], acc[i][j], 0, 0, 0);
+        }
+    };
+    Stage even, odd;
+    fetch(even, 0);
+    fetch(odd, C);
+    for (int k0 = 0; k0 < N; k0 += 2 * C) {
+        stage(even, buffers[0], k0);
+        stage(odd, buffers[1], k0 + C);   // past N: zeros
     }
+    __syncthreads();
+    store_tile<DT, BT, BM, WT, WM, WK>(acc, reinterpret_cast<int*>(buffers[0]), scale, x_scale, y, T, M, t0, m0);
 }
 
 }  // namespace gtokens
