@@ -59,6 +59,8 @@ class KvBatch(ctypes.Structure):
 def load():
     """Load the in-tree library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -401,15 +403,25 @@ def launch_plan_ptr(kind: str, A: int, scale: int, x: int, y: int, M: int, N: in
 
 # ---------------------------------------------------------------- several tokens, and the key-value cache
 # These take strided rows where the C ABI does, and make their outputs and
-# workspaces on the stream that the work runs on.
-def _work_stream(stream):
+# workspaces on the stream that the work runs on.  A decode step makes many
+# such calls, each shorter on the GPU than on the host, so the checks of a
+# right call are few steps: what fails them goes to _need for its reason.
+def _here():
+    import torch
+
+    get = getattr(torch._C, "_cuda_getDevice", None)   # current_device() without its check for a first use
+    return get() if get is not None else torch.cuda.current_device()
+
+
+def _work_stream(stream, device):
     """(handle, maker of empty tensors) of `stream`, or of the current stream."""
     import torch
 
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream, torch.empty
-    if stream.device.index != torch.cuda.current_device():
-        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{torch.cuda.current_device()}")
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # current_stream() without its wrapper object
+        return raw(device) if raw is not None else torch.cuda.current_stream().cuda_stream, torch.empty
+    if stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{device}")
 
     def empty(*args, **kw):
         # the allocator hands memory out by stream: what is freed when this
@@ -420,31 +432,48 @@ def _work_stream(stream):
     return stream.cuda_stream, empty
 
 
-def _rows(t, name, dtypes, shape):
-    """Data pointer and row stride of a device tensor whose rows are dense
-    (the rows themselves may lie apart)."""
+def _ptr(t, name, dtype, shape, device):
+    """Data pointer of a dense tensor of `dtype` and `shape` on `device`, the current one."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _need(t, name, (dtype,), shape)
+
+
+def _rows(t, name, dtype, shape, device, dense):
+    """Data pointer and row stride of a tensor whose rows, of `dense` elements
+    each, may lie apart."""
     import torch
 
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr(), dense
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.is_contiguous():
-        _need(t, name, dtypes, shape)
-        return t.data_ptr(), t[0].numel() if t.shape[0] else max(1, t.stride(0))
-    if t.dim() < 2 or t.stride(0) < 0 or not (t.shape[0] == 0 or t[0].is_contiguous()):
-        raise ValueError(f"{name}: the rows must be contiguous")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be a tensor of the current device, not of {t.device}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if tuple(t.shape) != tuple(shape):
+        return _need(t, name, (dtype,), shape), dense
+    if t.dim() < 2 or t.stride(0) < dense or not t[0].is_contiguous():
+        raise ValueError(f"{name}: the rows must be contiguous and not overlap")
+    _need(t[0], name, (dtype,), tuple(shape)[1:])
+    if t.shape != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     return t.data_ptr(), t.stride(0)
 
 
+_codes = {}
+
+
 def _code(dtype):
-    code = DTYPE.get(str(dtype)[6:])
+    code = _codes.get(dtype)
     if code is None:
-        raise TypeError(f"dtype {dtype} is none of {sorted(DTYPE)}")
+        code = DTYPE.get(str(dtype)[6:])   # "torch.float16"
+        if code is None:
+            raise TypeError(f"dtype {dtype} is none of {sorted(DTYPE)}")
+        _codes[dtype] = code
     return code
 
 
@@ -464,12 +493,13 @@ def quantize_tokens_q8(x, stream=None):
 
     T, N = x.shape
     _dims(T, N)
-    xp, stride = _rows(x, "x", (torch.float32, torch.float16, torch.bfloat16), (T, N))
-    handle, empty = _work_stream(stream)
+    here = _here()
+    code = _code(x.dtype)
+    xp, stride = _rows(x, "x", x.dtype, (T, N), here, N)
+    handle, empty = _work_stream(stream, here)
     q = empty((T, N), dtype=torch.int8, device=x.device)
     s = empty(T, dtype=torch.float32, device=x.device)
-    _check(quantize_tokens_q8_ptr(xp, _code(x.dtype), stride, q.data_ptr(), s.data_ptr(), T, N, handle),
-           "gemv_quantize_tokens_q8")
+    _check(quantize_tokens_q8_ptr(xp, code, stride, q.data_ptr(), s.data_ptr(), T, N, handle), "gemv_quantize_tokens_q8")
     return q, s
 
 
@@ -482,18 +512,24 @@ def gemm_q8(A, scale, x, x_scale, out=None, out_dtype=None, stream=None):
     M, N = A.shape
     T = x.shape[0]
     _dims(T, M, N)
-    a = _need(A, "A", (torch.int8,), (M, N))
-    s = _need(scale, "scale", (torch.float16, torch.int16, torch.uint16), (M,))
-    xp = _need(x, "x", (torch.int8,), (T, N))
-    xs = _need(x_scale, "x_scale", (torch.float32,), (T,))
-    handle, empty = _work_stream(stream)
+    here = _here()
+    a = _ptr(A, "A", torch.int8, (M, N), here)
+    s = _ptr(scale, "scale", torch.float16, (M,), here) if scale.dtype is torch.float16 else \
+        _need(scale, "scale", (torch.float16, torch.int16, torch.uint16), (M,))
+    xp = _ptr(x, "x", torch.int8, (T, N), here)
+    xs = _ptr(x_scale, "x_scale", torch.float32, (T,), here)
+    handle, empty = _work_stream(stream, here)
     if out is None:
-        out = empty((T, M), dtype=out_dtype or torch.float16, device=A.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    dtype = _code(out.dtype)
-    y = _need(out, "out", (out.dtype,), (T, M))
-    _check(gemm_q8_ptr(a, s, xp, xs, y, dtype, T, M, N, handle), "gemv_gemm_q8")
+        out_dtype = out_dtype or torch.float16
+        code = _code(out_dtype)
+        out = empty((T, M), dtype=out_dtype, device=A.device)
+        y = out.data_ptr()
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        code = _code(out.dtype)
+        y = _ptr(out, "out", out.dtype, (T, M), here)
+    _check(gemm_q8_ptr(a, s, xp, xs, y, code, T, M, N, handle), "gemv_gemm_q8")
     return out
 
 
@@ -525,7 +561,7 @@ class PagedCache:
         if dim < 8 or dim > 256 or dim % 8:
             raise ValueError(f"head_dim {dim} is no multiple of 8 from 8 to 256")
         # a dimension of size 1 is never stepped over: its stride is free
-        strides = [tuple(max(t.stride(d), dim) if t.shape[d] == 1 else t.stride(d) for d in range(3)) for t in (k, v)]
+        strides = [tuple(dim if t.shape[d] == 1 else t.stride(d) for d in range(3)) for t in (k, v)]
         if strides[0] != strides[1]:
             raise ValueError("k and v must have the same strides")
         if k.stride(3) != 1 or v.stride(3) != 1 or min(strides[0]) < dim:
@@ -534,30 +570,40 @@ class PagedCache:
             raise ValueError("k, v and their rows must be 16-byte aligned")
         self.k, self.v = k, v
         self.pages, self.page_size, self.heads, self.head_dim = pages, page_size, heads, dim
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
         self.c = KvCache(k.data_ptr(), v.data_ptr(), _code(k.dtype), pages, page_size, heads, dim, *strides[0])
+        self._by_ref = ctypes.byref(self.c)
+        self._needs = {}   # bytes of workspace by the shape of a call
 
-    def _batch(self, table, lens, max_len):
+    def _batch(self, table, lens, max_len, here):
         """gemv_kv_batch of a call, and the slots that its sequences may use."""
         import torch
 
-        if self.device.index != torch.cuda.current_device():
-            raise ValueError(f"the cache is on {self.device}, the current device is cuda:{torch.cuda.current_device()}")
+        if self.index != here:
+            raise ValueError(f"the cache is on {self.device}, the current device is cuda:{here}")
         B, width = table.shape
-        tp, stride = _rows(table, "table", (torch.int32,), (B, width))
-        lp = _need(lens, "lens", (torch.int32,), (B,))
+        tp, stride = _rows(table, "table", torch.int32, (B, width), here, width)
+        lp = _ptr(lens, "lens", torch.int32, (B,), here)
         room = min(width * self.page_size, _INT_MAX)
         if max_len is None:
             max_len = room
         if not 0 <= max_len <= _INT_MAX:
             raise ValueError(f"max_len {max_len} outside [0, 2^31 - 1]")
-        return KvBatch(tp, max(stride, width), width, lp, B, max_len), min(room, max_len)
+        return KvBatch(tp, stride, width, lp, B, max_len), min(room, max_len)
+
+    def _need(self, key, ask):
+        need = self._needs.get(key)
+        if need is None:
+            if len(self._needs) > 4096:
+                self._needs.clear()
+            need = self._needs[key] = ask()
+        return need
 
 
-def _tracked(t, name, dtype, batch, heads, room):
+def _tracked(t, name, dtype, batch, heads, room, here):
     if t.dim() != 3 or t.shape[2] < room:
         raise ValueError(f"{name} must be [batch, heads, slots] with at least {room} slots")
-    return _need(t, name, (dtype,), (batch, heads, t.shape[2]))
+    return _ptr(t, name, dtype, (batch, heads, t.shape[2]), here)
 
 
 def paged_attention(cache, table, lens, q, scale=None, max_len=None, weights=None, out=None, stream=None):
@@ -570,24 +616,28 @@ def paged_attention(cache, table, lens, q, scale=None, max_len=None, weights=Non
     summed over the query heads of its head, are added to it."""
     import torch
 
-    batch, room = cache._batch(table, lens, max_len)
+    here = _here()
+    batch, room = cache._batch(table, lens, max_len, here)
     B, heads, dim = q.shape
     if B != batch.batch or dim != cache.head_dim or heads < 1 or heads % cache.heads:
         raise ValueError(f"q: shape {tuple(q.shape)} does not fit {batch.batch} sequences, {cache.heads} heads of "
                          f"{cache.head_dim}")
-    qp, q_stride = _rows(q, "q", (cache.dtype,), (B, heads, dim))
-    handle, empty = _work_stream(stream)
+    qp, q_stride = _rows(q, "q", cache.dtype, (B, heads, dim), here, heads * dim)
+    handle, empty = _work_stream(stream, here)
     if out is None:
-        out = empty((B, heads, dim), dtype=cache.dtype, device=q.device)
-    op = _need(out, "out", (cache.dtype,), (B, heads, dim))
-    wp = None if weights is None else _tracked(weights, "weights", torch.float32, B, cache.heads, room)
-    slots = 0 if weights is None else weights.shape[2]
+        out = empty((B, heads, dim), dtype=cache.dtype, device=cache.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", cache.dtype, (B, heads, dim), here)
+    wp, slots = None, 0
+    if weights is not None:
+        wp, slots = _tracked(weights, "weights", torch.float32, B, cache.heads, room, here), weights.shape[2]
     scale = dim ** -0.5 if scale is None else scale
-    lib, c, s = load(), ctypes.byref(cache.c), ctypes.byref(batch)
-    need = lib.gemv_attention_workspace(c, s, heads, wp is not None)
-    work = empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _check(lib.gemv_attention(c, s, qp, max(q_stride, heads * dim), heads, scale, op, wp, slots,
-                              work.data_ptr() if need else None, need, handle), "gemv_attention")
+    lib, c, s = load(), cache._by_ref, ctypes.byref(batch)
+    need = cache._need((B, heads, room, wp is None), lambda: lib.gemv_attention_workspace(c, s, heads, wp is not None))
+    work = empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    _check(lib.gemv_attention(c, s, qp, q_stride, heads, scale, op, wp, slots, work.data_ptr() if need else None, need,
+                              handle), "gemv_attention")
     return out
 
 
@@ -600,26 +650,26 @@ def kv_append(cache, table, lens, starts, k, v, weights=None, positions=None, se
     the sequence's last tokens, of seen[b] in all."""
     import torch
 
-    batch, room = cache._batch(table, lens, None)
+    here = _here()
+    batch, _ = cache._batch(table, lens, None, here)
     B, rows = batch.batch, k.shape[0]
     _dims(rows)
-    shape = (rows, cache.heads, cache.head_dim)
-    kp, k_stride = _rows(k, "k", (cache.dtype,), shape)
-    vp, v_stride = _rows(v, "v", (cache.dtype,), shape)
-    sp = _need(starts, "starts", (torch.int32,), (B + 1,))
-    if len({weights is None, positions is None, seen is None}) != 1:
+    shape, dense = (rows, cache.heads, cache.head_dim), cache.heads * cache.head_dim
+    kp, k_stride = _rows(k, "k", cache.dtype, shape, here, dense)
+    vp, v_stride = _rows(v, "v", cache.dtype, shape, here, dense)
+    sp = _ptr(starts, "starts", torch.int32, (B + 1,), here)
+    if (weights is None) != (positions is None) or (weights is None) != (seen is None):
         raise ValueError("weights, positions and seen go together")
     wp = pp = np = None
     slots = 0
     if weights is not None:
-        slots = weights.shape[-1]
-        wp = _tracked(weights, "weights", torch.float32, B, cache.heads, 0)
-        pp = _need(positions, "positions", (torch.int32,), (B, cache.heads, slots))
-        np = _need(seen, "seen", (torch.int32,), (B,))
-    handle, _ = _work_stream(stream)
-    width = cache.heads * cache.head_dim
-    _check(load().gemv_kv_append(ctypes.byref(cache.c), ctypes.byref(batch), sp, kp, max(k_stride, width), vp,
-                                 max(v_stride, width), rows, wp, pp, np, slots, handle), "gemv_kv_append")
+        wp = _tracked(weights, "weights", torch.float32, B, cache.heads, 0, here)
+        slots = weights.shape[2]
+        pp = _ptr(positions, "positions", torch.int32, (B, cache.heads, slots), here)
+        np = _ptr(seen, "seen", torch.int32, (B,), here)
+    handle, _ = _work_stream(stream, here)
+    _check(load().gemv_kv_append(cache._by_ref, ctypes.byref(batch), sp, kp, k_stride, vp, v_stride, rows, wp, pp, np,
+                                 slots, handle), "gemv_kv_append")
 
 
 def kv_evict(cache, table, lens, seen, weights, positions, budget, recent, max_len=None, out=None, stream=None):
@@ -631,26 +681,29 @@ def kv_evict(cache, table, lens, seen, weights, positions, budget, recent, max_l
     ``out``, (weights, positions, lens) afterwards."""
     import torch
 
-    batch, room = cache._batch(table, lens, max_len)
+    here = _here()
+    batch, room = cache._batch(table, lens, max_len, here)
     B = batch.batch
-    wp = _tracked(weights, "weights", torch.float32, B, cache.heads, room)
-    slots = weights.shape[2]
-    pp = _need(positions, "positions", (torch.int32,), (B, cache.heads, slots))
-    np = _need(seen, "seen", (torch.int32,), (B,))
+    wp = _tracked(weights, "weights", torch.float32, B, cache.heads, room, here)
+    shape = weights.shape
+    pp = _ptr(positions, "positions", torch.int32, shape, here)
+    np = _ptr(seen, "seen", torch.int32, (B,), here)
     _dims(budget, recent)
-    handle, empty = _work_stream(stream)
+    handle, empty = _work_stream(stream, here)
     if out is None:
-        out = (empty(weights.shape, dtype=torch.float32, device=weights.device),
-               empty(weights.shape, dtype=torch.int32, device=weights.device),
-               empty(B, dtype=torch.int32, device=weights.device))
-    new_w, new_p, left = out
-    outs = (_need(new_w, "out[0]", (torch.float32,), weights.shape), _need(new_p, "out[1]", (torch.int32,), weights.shape),
-            _need(left, "out[2]", (torch.int32,), (B,)))
-    if weights.numel() and (outs[0] == wp or outs[1] == pp) or B and outs[2] == batch.lens:
-        raise ValueError("the outputs must not be the inputs")
-    lib, c, s = load(), ctypes.byref(cache.c), ctypes.byref(batch)
-    need = lib.gemv_kv_evict_workspace(c, s, budget)
-    work = empty(max(need, 16), dtype=torch.uint8, device=weights.device)
-    _check(lib.gemv_kv_evict(c, s, np, wp, pp, slots, budget, recent, *outs, work.data_ptr(), need, handle),
-           "gemv_kv_evict")
+        new_w = empty(shape, dtype=torch.float32, device=cache.device)
+        new_p = empty(shape, dtype=torch.int32, device=cache.device)
+        left = empty(B, dtype=torch.int32, device=cache.device)
+        outs = new_w.data_ptr(), new_p.data_ptr(), left.data_ptr()
+    else:
+        new_w, new_p, left = out
+        outs = (_ptr(new_w, "out[0]", torch.float32, shape, here), _ptr(new_p, "out[1]", torch.int32, shape, here),
+                _ptr(left, "out[2]", torch.int32, (B,), here))
+        if weights.numel() and (outs[0] == wp or outs[1] == pp) or B and outs[2] == batch.lens:
+            raise ValueError("the outputs must not be the inputs")
+    lib, c, s = load(), cache._by_ref, ctypes.byref(batch)
+    need = cache._need((B, budget, room), lambda: lib.gemv_kv_evict_workspace(c, s, budget))
+    work = empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    _check(lib.gemv_kv_evict(c, s, np, wp, pp, shape[2], budget, recent, *outs, work.data_ptr() if need else None, need,
+                             handle), "gemv_kv_evict")
     return new_w, new_p, left

@@ -51,9 +51,9 @@ int check(const gemv_kv_cache* c, const gemv_kv_batch* s, Pages* out)
     return GEMV_OK;
 }
 
-int launch(const void* fn, int64_t grid, int block, void** args, hipStream_t stream)
+int launch(const void* fn, int64_t grid, int block, void** args, hipStream_t stream, int lds = 0)
 {
-    return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(block), args, 0, stream) == hipSuccess ? GEMV_OK
+    return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(block), args, lds, stream) == hipSuccess ? GEMV_OK
                                                                                                  : GEMV_E_LAUNCH;
 }
 
@@ -120,10 +120,24 @@ int evict_moves(int limit, int budget)
     return over < budget ? over : budget;
 }
 
-size_t evict_bytes(int batch, int heads, int moves)
+// The workspace of an eviction: what the selection leaves for the launch that
+// moves, nothing where it moves by itself.
+struct Scratch {
+    int words;
+    size_t bits_at, moves_at, bytes;
+};
+
+Scratch evict_scratch(int batch, int heads, int limit, int budget, int moves)
 {
+    Scratch s{};
+    if (moves <= kFusedMoves)
+        return s;
     const size_t bh = (size_t)batch * (size_t)heads;
-    return round16(bh * sizeof(int32_t)) + bh * 2 * (size_t)moves * sizeof(int32_t);
+    s.words = ((budget < limit ? budget : limit) + 63) / 64;
+    s.bits_at = round16(bh * sizeof(int32_t));
+    s.moves_at = s.bits_at + round16(bh * s.words * sizeof(uint64_t));
+    s.bytes = s.moves_at + bh * 2 * (size_t)moves * sizeof(int32_t);
+    return s;
 }
 
 }  // namespace
@@ -260,7 +274,7 @@ size_t gemv_kv_evict_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* 
     Pages at{};
     if (check(cache, batch, &at) != GEMV_OK || budget < 0)
         return 0;
-    return evict_bytes(batch->batch, cache->heads, evict_moves(at.limit, budget));
+    return evict_scratch(batch->batch, cache->heads, at.limit, budget, evict_moves(at.limit, budget)).bytes;
 }
 
 int gemv_kv_evict(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* seen, const float* weights,
@@ -283,12 +297,13 @@ int gemv_kv_evict(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const 
     if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
         return rc;
     a.moves_max = evict_moves(a.at.limit, budget);
-    const size_t bytes = evict_bytes(batch->batch, cache->heads, a.moves_max);
-    if (workspace == nullptr || workspace_bytes < bytes || !aligned(workspace, 16))
+    const Scratch ws = evict_scratch(batch->batch, cache->heads, a.at.limit, budget, a.moves_max);
+    if (ws.bytes > 0 && (workspace == nullptr || workspace_bytes < ws.bytes || !aligned(workspace, 16)))
         return GEMV_E_INVAL;
     const int64_t items = (int64_t)batch->batch * cache->heads;
-    int blocks = (a.moves_max + 31) / 32;   // eight moves a wave
-    blocks = blocks > 256 ? 256 : blocks;
+    // two pieces a thread; a move has head_dim / 4 of them
+    int blocks = (int)(((int64_t)a.moves_max * (cache->head_dim / 4) + 511) / 512);
+    blocks = blocks > 1024 ? 1024 : blocks;
     if (!fits(items, kEvictThreads) || !fits(items * blocks, 256))
         return GEMV_E_UNSUPPORTED;
     a.k = static_cast<uint16_t*>(cache->k);
@@ -304,11 +319,18 @@ int gemv_kv_evict(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const 
     a.weights_out = weights_out;
     a.positions_out = positions_out;
     a.lens_out = lens_out;
-    a.count = static_cast<int32_t*>(workspace);
-    a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + round16((size_t)items * sizeof(int32_t)));
+    char* at = static_cast<char*>(workspace);
+    a.words = ws.words;
+    a.count = reinterpret_cast<int32_t*>(at);
+    a.bits = reinterpret_cast<uint64_t*>(at + ws.bits_at);
+    a.moves = reinterpret_cast<int32_t*>(at + ws.moves_at);
     void* args[] = {(void*)&a};
-    if (int rc = launch(reinterpret_cast<const void*>(&evict_select_kernel), items, kEvictThreads, args, stream);
-        rc != GEMV_OK || blocks == 0)
+    const bool fused = a.moves_max <= kFusedMoves;
+    a.held = a.at.limit < kHeldKeys ? a.at.limit : kHeldKeys;
+    if (int rc = launch(fused ? reinterpret_cast<const void*>(&evict_select_kernel<true>)
+                              : reinterpret_cast<const void*>(&evict_select_kernel<false>),
+                        items, kEvictThreads, args, stream, a.held * (int)sizeof(unsigned));
+        rc != GEMV_OK || fused)
         return rc;
     void* margs[] = {(void*)&a, (void*)&blocks};
     return launch(reinterpret_cast<const void*>(&evict_move_kernel), items * blocks, 256, margs, stream);
