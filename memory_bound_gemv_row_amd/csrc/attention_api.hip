@@ -61,10 +61,14 @@ bool fits(int64_t grid, int block) { return grid <= gemv_device::kMaxWorkItems /
 
 // How the length is split: workgroups per key-value head and slots of each.
 struct Split {
+    bool lone;
     int tiles, parts, chunk;
     int64_t logits_stride;
     size_t ms_at, out_at, logits_at, bytes;
 };
+
+// Tiles of 16 slots that lie in one page, near enough for 32-bit offsets.
+bool whole_tiles(const gemv_kv_cache* c) { return c->page_size % 16 == 0 && c->stride_slot < (1 << 26); }
 
 // The length is cut into parts so that there are about four workgroups per
 // CU, of 64 slots (a tile for each wave) to 1024: where lengths are ragged,
@@ -78,6 +82,14 @@ Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q
     int64_t chunk = items > 0 ? (int64_t)limit * items / ((int64_t)cus * 4) : limit;
     chunk = (chunk + 63) / 64 * 64;
     chunk = chunk < 64 ? 64 : (chunk > kMaxChunk ? kMaxChunk : chunk);
+    // Short lengths are not split: eight waves of one workgroup are done before
+    // a second launch has joined parts.  Head size 128, in a captured graph: 8
+    // key-value heads of 256 slots 7.5 us against 9.5, of 512 slots 11.3 against
+    // 8.8; 128 of them, which fill half the card, 512 slots 12.3 against 17.6, 768
+    // 15.8 against 16.7.
+    p.lone = whole_tiles(c) && chunk < limit && (limit <= 256 || (limit <= 768 && items * 2 >= cus));
+    if (p.lone)
+        chunk = (limit + 63) / 64 * 64;
     p.chunk = (int)chunk;
     p.parts = (int)(((int64_t)limit + p.chunk - 1) / p.chunk);
     p.parts = p.parts < 1 ? 1 : p.parts;
@@ -90,28 +102,28 @@ Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q
     return p;
 }
 
-template <int DT, bool WHOLE>
+template <int DT, bool WHOLE, int WAVES>
 const void* attention_sized(int dim)
 {
     if constexpr (WHOLE) {
         if (dim == 64)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 64, true, true>);
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 64, true, true, WAVES>);
         if (dim == 128)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 128, true, true>);
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 128, true, true, WAVES>);
         if (dim == 256)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 256, true, true>);
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 256, true, true, WAVES>);
     }
-    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64, WHOLE, false>)
-           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128, WHOLE, false>)
-                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256, WHOLE, false>);
+    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64, WHOLE, false, WAVES>)
+           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128, WHOLE, false, WAVES>)
+                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256, WHOLE, false, WAVES>);
 }
 
-const void* attention_for(const gemv_kv_cache* c)
+template <int DT>
+const void* attention_for(const gemv_kv_cache* c, bool lone)
 {
-    const bool whole = c->page_size % 16 == 0 && c->stride_slot < (1 << 26);
-    if (c->dtype == GEMV_F16)
-        return whole ? attention_sized<kF16, true>(c->head_dim) : attention_sized<kF16, false>(c->head_dim);
-    return whole ? attention_sized<kBF16, true>(c->head_dim) : attention_sized<kBF16, false>(c->head_dim);
+    return lone             ? attention_sized<DT, true, kLoneWaves>(c->head_dim)
+           : whole_tiles(c) ? attention_sized<DT, true, kWaves>(c->head_dim)
+                            : attention_sized<DT, false, kWaves>(c->head_dim);
 }
 
 int evict_moves(int limit, int budget)
@@ -185,7 +197,7 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
     const int64_t grid = cache->heads * (p.tiles > 1 ? (ranges + 7) / 8 * 8 * p.tiles : ranges);
     const int64_t joins = p.parts > 1 ? (int64_t)batch->batch * q_heads : 0;
     int blocks = weights != nullptr ? (int)(((int64_t)a.at.limit + 1023) / 1024) : 0;
-    if (!fits(grid, kWaves * 64) || !fits(joins + items * blocks, 256))
+    if (!fits(grid, kLoneWaves * 64) || !fits(joins + items * blocks, 256))
         return GEMV_E_UNSUPPORTED;
     char* ws = static_cast<char*>(workspace);
     a.k = static_cast<const uint16_t*>(cache->k);
@@ -210,7 +222,9 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
     a.slots = slots;
     a.weights_wide = slots % 4 == 0 && aligned(weights, 16);
     void* args[] = {(void*)&a};
-    if (int rc = launch(attention_for(cache), grid, kWaves * 64, args, stream); rc != GEMV_OK)
+    const void* fn = cache->dtype == GEMV_F16 ? attention_for<kF16>(cache, p.lone) : attention_for<kBF16>(cache, p.lone);
+    const int block = (p.lone ? kLoneWaves : kWaves) * 64;
+    if (int rc = launch(fn, grid, block, args, stream); rc != GEMV_OK)
         return rc;
     if (joins + items * blocks == 0)
         return GEMV_OK;

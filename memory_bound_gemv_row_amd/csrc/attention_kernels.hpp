@@ -115,7 +115,8 @@ __device__ __forceinline__ float part_factor(float m, float s, float top)
     return m == -kInf ? (s == 0.0f ? 0.0f : 1.0f) : exp2_hw(m - top);
 }
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;         // of a workgroup, where the length is split or the card is full
+constexpr int kLoneWaves = 8;     // where one workgroup takes a short sequence's whole length
 constexpr int kMaxChunk = 1024;  // slots of a part: 16 tiles a wave
 constexpr float kSlack = 8.0f;   // powers of two that a logit may pass the reference maximum by
 
@@ -152,17 +153,17 @@ __device__ __forceinline__ Buffer buffer(const uint16_t* p, unsigned bytes)
 // pages are whole numbers of tiles (WHOLE), a tile has one page and its
 // address is the same for all lanes; otherwise each row has an address of its
 // own.  EXACT: the head's size is DP, so no lane is without an element.
-template <int DT, int DP, bool WHOLE, bool EXACT>
-__global__ void __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2)
+template <int DT, int DP, bool WHOLE, bool EXACT, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, DP == 256 ? 1 : 2)
 attention_kernel(Attention a)
 {
     constexpr int kSteps = DP / 32;              // of 32 elements of the dot products
     constexpr int VW = DP == 64 ? 4 : 8;         // elements of a value row per lane and set
     constexpr int kSets = DP / (16 * VW);
     constexpr int kWords = VW / 2;
-    __shared__ float red_m[kWaves][16];
-    __shared__ float red_s[kWaves][16];
-    __shared__ float red_o[kWaves][16][DP];
+    __shared__ float red_m[WAVES][16];
+    __shared__ float red_s[WAVES][16];
+    __shared__ float red_o[WAVES][16][DP];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -218,7 +219,7 @@ attention_kernel(Attention a)
         unsigned value[4][kSets][kWords];
         unsigned held;   // bit r: slot 4 quarter + r is there
     };
-    auto slot_of = [&](int t) { return begin + (wave + t * kWaves) * 16; };   // tile t of this wave
+    auto slot_of = [&](int t) { return begin + (wave + t * WAVES) * 16; };   // tile t of this wave
     const uint16_t* k0 = a.k + kv * a.at.stride_head;
     const uint16_t* v0 = a.v + kv * a.at.stride_head;
 
@@ -227,11 +228,11 @@ attention_kernel(Attention a)
     int pages = -1;
     __shared__ int32_t slot_page[WHOLE ? 1 : kMaxChunk];
     if constexpr (WHOLE) {
-        const int64_t j = (int64_t)begin + (wave + lane * kWaves) * 16;
+        const int64_t j = (int64_t)begin + (wave + lane * WAVES) * 16;
         if (j < a.at.limit)
             pages = a.at.table[b * a.at.table_stride + a.at.page_of.by((int)j)];
     } else {
-        for (int i = threadIdx.x; i < a.chunk; i += kWaves * 64)
+        for (int i = threadIdx.x; i < a.chunk; i += WAVES * 64)
             slot_page[i] = begin + i < end ? a.at.table[b * a.at.table_stride + a.at.page_of.by(begin + i)] : -1;
         __syncthreads();
     }
@@ -386,17 +387,17 @@ attention_kernel(Attention a)
                 for (int e = 0; e < VW; ++e)
                     red_o[wave][4 * quarter + r][16 * VW * s + VW * col + e] = acc[s][e][r];
     __syncthreads();
-    for (int i = threadIdx.x; i < nheads * DP; i += kWaves * 64) {
+    for (int i = threadIdx.x; i < nheads * DP; i += WAVES * 64) {
         const int h = i / DP, d = i % DP;
         if (!EXACT && d >= a.dim)
             continue;
         float top = -kInf;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
+        for (int w = 0; w < WAVES; ++w)
             top = fmaxf(top, red_m[w][h]);
         float o = 0.0f, total = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             const float f = part_factor(red_m[w][h], red_s[w][h], top);
             o += f * red_o[w][h][d];
             total += f * red_s[w][h];
