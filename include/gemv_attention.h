@@ -17,8 +17,8 @@
  *
  * Nothing on the device is trusted for addressing: a page number outside
  * [0, pages) is a hole (its slots are not read, written or attended to), a
- * length is taken as at most max_len and the table's width, a negative one
- * as 0.
+ * length is taken as at most max_len, the table's width and 2^31 - 4096, a
+ * negative one as 0.
  *
  * Addressing needs 16-byte-aligned keys and values: k, v and every row, so
  * strides and head_dim are multiples of 8 elements; GEMV_E_UNSUPPORTED
@@ -66,13 +66,14 @@ typedef struct gemv_kv_batch {
  *   q     [batch][q_heads][head_dim] of the cache's type, sequences q_stride
  *         elements apart (a multiple of 8); q_heads a multiple of heads;
  *   out   [batch][q_heads][head_dim] of the cache's type, dense.
- * A sequence of length 0, or with holes only, gets zeros.  Products are
- * summed and the softmax is taken in binary32.
+ * A sequence of length 0, with holes only, or with no logit above -inf gets
+ * zeros.  Products are summed and the softmax is taken in binary32; the
+ * probabilities are not rounded before they meet the values.
  * `weights`, if not NULL: float [batch][heads][slots], slots >= max_len;
  *   weights[b][h'][j] += sum over the query heads h of h' of p_bhj, j < lens[b]
  * (0 for holes); other entries stay as they are.
- * The length is split over workgroups where there are few sequences; the
- * parts are joined in order of position. */
+ * Lengths are split over workgroups, and the parts joined in order of
+ * position, in a second launch; short ones are not split. */
 size_t gemv_attention_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* batch, int q_heads, int weighted);
 
 int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const void* q, int64_t q_stride,

@@ -47,7 +47,7 @@ int gemv_quantize_tokens_q8(const void* x, int dtype, int64_t stride, int8_t* q,
  * 131071, where no sum can leave 32 bits (GEMV_E_UNSUPPORTED beyond).
  * N == 0 writes products of zero.  M == 0 or T == 0 is a no-op.
  * The bandwidth path needs 16-byte-aligned A and x and N % 16 == 0; others
- * take a slower path. */
+ * take a slower path, whose operands go through registers. */
 int gemv_gemm_q8(const int8_t* A, const uint16_t* scale, const int8_t* x, const float* x_scale, void* y, int dtype,
                  int T, int M, int N, hipStream_t stream);
 

@@ -44,8 +44,10 @@ int check(const gemv_kv_cache* c, const gemv_kv_batch* s, Pages* out)
     if (c->head_dim % 8 != 0 || c->head_dim > 256 || c->stride_page % 8 != 0 || c->stride_slot % 8 != 0 ||
         c->stride_head % 8 != 0 || !aligned(c->k, 16) || !aligned(c->v, 16))
         return GEMV_E_UNSUPPORTED;
-    const int64_t room = (int64_t)s->width * c->page_size;
-    const int64_t limit = room < s->max_len ? room : s->max_len;
+    // the kernels step past a length by up to a few thousand slots, in int
+    const int64_t room = (int64_t)s->width * c->page_size, most = INT_MAX - 4095;
+    int64_t limit = room < s->max_len ? room : s->max_len;
+    limit = limit < most ? limit : most;
     *out = Pages{s->table, s->table_stride, s->lens, (int)limit, c->pages, c->page_size, divider(c->page_size),
                  c->stride_page, c->stride_slot, c->stride_head};
     return GEMV_OK;

@@ -92,7 +92,7 @@ def attention(pool, q, scale):
     multiplied twice and subtracted once; its absolute error e makes the
     power's relative error e, taken twice (numerator and sum).  exp2 is good to
     two units in the last place.  A wave's sums run over at most a quarter of
-    the length in tiles of 16, then 4 waves and at most len / 256 + 1 parts
+    the length in tiles of 16, then 4 or 8 waves and at most len / 64 + 1 parts
     are added; the division and the output's rounding come last."""
     B, Hq, D = q.shape
     H, G = pool.heads, Hq // pool.heads
@@ -114,7 +114,7 @@ def attention(pool, q, scale):
                 p = np.exp(x - x.max())
                 p /= p.sum()
                 e = (2 * D * U32 * mag + 6 * U32 * (np.abs(np.where(held, x, 0)) + np.abs(x[held]).max()))[held].max()
-                sums = (16 * -(-n // 64) + 4 + n // 256 + 2) * U32
+                sums = (16 * -(-n // 64) + 8 + n // 64 + 1) * U32
                 rel = 2 * np.expm1(e) + 8 * U32 + 2 * sums
                 o = p @ np.where(held[:, None], v, 0)
                 out[b, h * G + g] = o

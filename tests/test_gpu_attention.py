@@ -511,3 +511,108 @@ def test_refusals(gpu):
                 lambda: binding.kv_evict(cache, table, lens, lens, w, pos, 8, 0, out=(w, pos, lens))):
         with pytest.raises((ValueError, TypeError, binding.GemvError)):
             bad()
+
+
+# ---------------------------------------------------------------- edges of the calls
+def test_no_sequences_no_slots_no_rows(gpu):
+    pool = ref.Pool([20, 20], 2, 64, 16, seed=1)
+    cache = binding.PagedCache(pool.dk, pool.dv)
+    q = _query(2, 4, 64, torch.float16, 1).cuda()
+    w = torch.ones((2, 2, 32), device="cuda")
+    pos = torch.zeros((2, 2, 32), dtype=torch.int32, device="cuda")
+    say("[attention] nothing to attend to")
+    assert torch.all(binding.paged_attention(cache, pool.dtable, pool.dlens, q, max_len=0, weights=w) == 0)
+    assert torch.all(binding.paged_attention(cache, pool.dtable[:, :0], pool.dlens, q) == 0)
+    assert torch.all(w == 1)
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert binding.paged_attention(cache, pool.dtable[:0], none, q[:0]).shape == (0, 4, 64)
+    starts = torch.zeros(3, dtype=torch.int32, device="cuda")
+    binding.kv_append(cache, pool.dtable, pool.dlens, starts, q[:0, :2], q[:0, :2])
+    new_w, new_p, left = binding.kv_evict(cache, pool.dtable, pool.dlens, pool.dlens, w, pos, 4, 0, max_len=0)
+    assert torch.all(new_w == 0) and torch.all(new_p == -1) and torch.all(left == 0)
+    new_w, _, left = binding.kv_evict(cache, pool.dtable[:0], none, none, w[:0], pos[:0], 4, 0)
+    assert new_w.shape == (0, 2, 32) and left.shape == (0,)
+    empty = binding.PagedCache(pool.dk[:0], pool.dv[:0])      # a pool without pages: every page is a hole
+    assert torch.all(binding.paged_attention(empty, pool.dtable, pool.dlens, q) == 0)
+    assert _same(pool.dk.cpu(), pool.k)
+
+
+@pytest.mark.parametrize("budget,recent", [(5000, 300), (39990, 64), (39998, 0), (20000, 25000)])
+def test_evict_past_the_held_keys(gpu, budget, recent):
+    # more slots than LDS holds keys of
+    _check_evict([40000, 33000], 1, 8, 64, budget, recent, seed=budget, ties=budget == 5000)
+
+
+@pytest.mark.parametrize("few", [1, 2, 3, 4, 5])
+def test_evict_few_among_equals(gpu, few):
+    # the last of equals go first, newest or not
+    rng = np.random.default_rng(few)
+    for recent in (0, 3, 64):
+        n, budget = 64 + few, 64
+        pool = ref.Pool([n], 1, 8, 16, torch.float16, seed=few)
+        w = np.zeros((1, 1, pool.width * 16), np.float32)
+        w[0, 0, : n // 2] = rng.integers(0, 2, n // 2)
+        pos = np.arange(pool.width * 16, dtype=np.int32).reshape(1, 1, -1)
+        source, want_w, want_p, _ = ref.evict([n], [n], w, pos, budget, recent, w.shape[2])
+        seen = torch.tensor([n], dtype=torch.int32, device="cuda")
+        new_w, new_p, _ = binding.kv_evict(binding.PagedCache(pool.dk, pool.dv), pool.dtable, pool.dlens, seen,
+                                           torch.from_numpy(w).cuda(), torch.from_numpy(pos).cuda(), budget, recent)
+        assert np.array_equal(new_w.cpu().numpy(), want_w) and np.array_equal(new_p.cpu().numpy(), want_p)
+
+
+# whole and cut lengths on both sides of the rules that choose how a length is shared out
+@pytest.mark.parametrize("n", [256, 257, 320, 511, 512, 767, 768, 769, 1023, 1025, 2049])
+def test_sharing_of_lengths(gpu, n):
+    for B, kv in ((1, 1), (3, 4), (33, 4)):
+        lens = [n] + [1 + (n * i) // B for i in range(1, B)]
+        pool = ref.Pool(lens if B < 33 else [n, 1, 17] * 11, kv, 8, 16, seed=n)
+        _check(pool, _query(B, kv * 2, 8, torch.float16, n), f"{B} of up to {n}, {kv} heads", weighted=B < 33)
+
+
+def test_many_query_heads_over_long_lengths(gpu):
+    # several sets of 16 query heads read the same keys, in padded groups of workgroups
+    pool = ref.Pool([1500, 700, 1499], 1, 16, 16, seed=21)
+    _check(pool, _query(3, 40, 16, torch.float16, 21), "40 heads over 1")
+    pool = ref.Pool([1500, 700, 1499], 2, 16, 24, seed=22)
+    _check(pool, _query(3, 34, 16, torch.float16, 22), "34 heads over 2, loose pages")
+
+
+def test_first_call_inside_graph_capture(gpu):
+    # a fresh process whose first calls of these operators are captured
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from memory_bound_gemv_row_amd import binding as B
+g = torch.Generator(device="cuda").manual_seed(1)
+k = torch.randn((40, 16, 2, 64), generator=g, device="cuda").half()
+c = B.PagedCache(k, k.clone())
+t = torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20)
+n = torch.tensor([300, 20], dtype=torch.int32, device="cuda")
+q = torch.randn((2, 8, 64), generator=g, device="cuda").half()
+w = torch.rand((2, 2, 320), generator=g, device="cuda")
+p = torch.arange(320, dtype=torch.int32, device="cuda").expand(2, 2, 320).contiguous()
+A = torch.randint(-127, 128, (96, 512), generator=g, device="cuda", dtype=torch.int8)
+s = torch.rand(96, generator=g, device="cuda").half()
+torch.cuda.synchronize()
+def work():
+    x, xs = B.quantize_tokens_q8(q.view(2, 512))
+    return [B.gemm_q8(A, s, x, xs), B.paged_attention(c, t, n, q), *B.kv_evict(c, t, n, n, w, p, 100, 10)]
+graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+    outs = work()
+torch.cuda.synchronize()
+graph.replay()      # its eviction moves rows; later passes find the cache so
+torch.cuda.synchronize()
+graph.replay()
+torch.cuda.synchronize()
+got = [o.clone() for o in outs]
+assert all(torch.equal(a, b) for a, b in zip(got, work()))
+print("first-call capture ok", flush=True)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    say("[serving graph] first call captured, fresh process")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "first-call capture ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]

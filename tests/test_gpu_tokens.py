@@ -230,3 +230,23 @@ def test_refusals(gpu):
     with pytest.raises(binding.GemvError) as e:
         binding.gemm_q8(big, torch.ones(1, dtype=torch.float16, device="cuda"), big, torch.ones(1, device="cuda"))
     assert e.value.status == 2
+
+
+def test_large_tiles_whole_and_halved(gpu):
+    # tiles of 256 x 256: fewer than the CUs, whole rounds of them, and rounds
+    # whose rest is done in halves, one of which may lie past the last output
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 256 * 16
+    for tiles_m, short in ((cus * 3 // 4 // 16 + 1, 100), (cus // 16, 0), (cus // 16 + 2, 0), (cus // 16 + 3, 200),
+                           (cus // 16 + 9, 128)):
+        M, N = tiles_m * 256 - short, 208
+        A, s, x, xs = _operands(rows - 7, M, N, tiles_m)
+        _check_product(A, s, x, xs, torch.float16, f"{rows - 7}x{M}x{N}")
+
+
+def test_few_tokens_at_every_tiling(gpu):
+    # outputs and tokens such that each tile size is the cheapest once, with
+    # columns that end inside a stage
+    for T, M, N in ((1, 300, 1040), (5, 4096, 528), (16, 9000, 528), (20, 4000, 272), (32, 9000, 272), (30, 20000, 144),
+                    (60, 4000, 528), (64, 20000, 144), (128, 4000, 400), (120, 14336, 144), (300, 8192, 144)):
+        _check_product(*_operands(T, M, N, T), torch.bfloat16, f"T={T} M={M} N={N}")
