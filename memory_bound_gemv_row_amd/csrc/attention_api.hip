@@ -72,18 +72,41 @@ struct Split {
 // Tiles of 16 slots that lie in one page, near enough for 32-bit offsets.
 bool whole_tiles(const gemv_kv_cache* c) { return c->page_size % 16 == 0 && c->stride_slot < (1 << 26); }
 
-// The length is cut into parts so that there are about four workgroups per
-// CU, of 64 slots (a tile for each wave) to 1024: where lengths are ragged,
-// short parts even out what the CUs get.
+// Slots of a part, a multiple of 64 (a tile for each wave) up to kMaxChunk.
+// Head sizes up to 64 have small tiles and wait for them: eight workgroups per
+// CU (16 heads of 64, 16 x 301 to 2047 slots: 24.5 us; with two 25.7, with one
+// 28.9).  Others run at the card's bandwidth with one workgroup per CU, and a
+// second round that is mostly empty costs most: the least estimate, in slots,
+// of what the busiest CU reads, with 100 for a workgroup's start and end and
+// 150 for a join.  8 key-value heads of 128, 2 x 8192 slots: 18.3 us, with two
+// workgroups per CU 21.2, with four 24.0; 32 x 1024: 24.7, 31.1, 30.9; 5 heads of
+// 96, 32 x 2000: three parts; one, two and four per CU 41.3, 34.8, 37.6.
+int chunk_for(int64_t items, int limit, int dim, int cus)
+{
+    if (dim <= 64) {
+        const int64_t chunk = ((int64_t)limit * items / ((int64_t)cus * 8) + 63) / 64 * 64;
+        return (int)(chunk < 64 ? 64 : (chunk > kMaxChunk ? kMaxChunk : chunk));
+    }
+    int best = kMaxChunk;
+    int64_t least = INT64_MAX;
+    for (int chunk = kMaxChunk; chunk >= 64; chunk -= 64) {
+        const int64_t parts = ((int64_t)limit + chunk - 1) / chunk;
+        const int64_t cost = (items * parts + cus - 1) / cus * (chunk + 100) + (parts > 1 ? 150 + parts : 0);
+        if (cost < least) {
+            best = chunk;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q_heads, bool weighted, int cus)
 {
     Split p;
     const int group = q_heads / c->heads;
     p.tiles = (group + 15) / 16;
     const int64_t items = (int64_t)s->batch * c->heads * p.tiles;
-    int64_t chunk = items > 0 ? (int64_t)limit * items / ((int64_t)cus * 4) : limit;
-    chunk = (chunk + 63) / 64 * 64;
-    chunk = chunk < 64 ? 64 : (chunk > kMaxChunk ? kMaxChunk : chunk);
+    int chunk = chunk_for(items, limit, c->head_dim, cus);
     // Short lengths are not split: eight waves of one workgroup are done before
     // a second launch has joined parts.  Head size 128, in a captured graph: 8
     // key-value heads of 256 slots 7.5 us against 9.5, of 512 slots 11.3 against
@@ -92,7 +115,7 @@ Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q
     p.lone = whole_tiles(c) && chunk < limit && (limit <= 256 || (limit <= 768 && items * 2 >= cus));
     if (p.lone)
         chunk = (limit + 63) / 64 * 64;
-    p.chunk = (int)chunk;
+    p.chunk = chunk;
     p.parts = (int)(((int64_t)limit + p.chunk - 1) / p.chunk);
     p.parts = p.parts < 1 ? 1 : p.parts;
     const size_t rows = (size_t)s->batch * (size_t)q_heads;
