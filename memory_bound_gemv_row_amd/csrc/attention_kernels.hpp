@@ -173,7 +173,7 @@ attention_kernel(Attention a)
     constexpr int kWords = VW / 2;
     __shared__ float red_m[WAVES][16];
     __shared__ float red_s[WAVES][16];
-    __shared__ float red_o[WAVES][16][DP];
+    __shared__ __attribute__((aligned(16))) float red_o[WAVES][16][DP];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -397,30 +397,44 @@ attention_kernel(Attention a)
                 for (int e = 0; e < VW; ++e)
                     red_o[wave][4 * quarter + r][16 * VW * s + VW * col + e] = acc[s][e][r];
     __syncthreads();
-    for (int i = threadIdx.x; i < nheads * DP; i += WAVES * 64) {
-        const int h = i / DP, d = i % DP;
-        if (!EXACT && d >= a.dim)
-            continue;
-        float top = -kInf;
+    // a wave's factor for a head, once, then four elements a thread
+    if (threadIdx.x < 16) {
+        const int h = threadIdx.x;
+        float top = -kInf, total = 0.0f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w)
             top = fmaxf(top, red_m[w][h]);
-        float o = 0.0f, total = 0.0f;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const float f = part_factor(red_m[w][h], red_s[w][h], top);
-            o += f * red_o[w][h][d];
             total += f * red_s[w][h];
+            red_m[w][h] = f;
         }
-        const int64_t row = (int64_t)b * a.q_heads + head0 + h;
-        if (a.part_ms != nullptr && d == 0) {
+        red_s[0][h] = total;
+        if (a.part_ms != nullptr && h < nheads) {
+            const int64_t row = (int64_t)b * a.q_heads + head0 + h;
             a.part_ms[(row * a.parts + part) * 2] = top;
             a.part_ms[(row * a.parts + part) * 2 + 1] = total;
         }
-        if (a.parts > 1)
-            a.part_out[(row * a.parts + part) * a.dim + d] = o;
-        else
-            narrow_to<DT>(a.out, row * a.dim + d, total == 0.0f ? 0.0f : o / total);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < nheads * (DP / 4); i += WAVES * 64) {
+        const int h = i / (DP / 4), d = i % (DP / 4) * 4;
+        if (!EXACT && d >= a.dim)
+            continue;
+        f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            o += red_m[w][h] * *reinterpret_cast<const f32x4*>(&red_o[w][h][d]);
+        const int64_t row = (int64_t)b * a.q_heads + head0 + h;
+        if (a.parts > 1) {
+            *reinterpret_cast<f32x4*>(a.part_out + (row * a.parts + part) * a.dim + d) = o;
+        } else {
+            const float total = red_s[0][h];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                narrow_to<DT>(a.out, row * a.dim + d + k, total == 0.0f ? 0.0f : o[k] / total);
+        }
     }
 }
 
