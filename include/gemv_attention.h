@@ -73,7 +73,10 @@ typedef struct gemv_kv_batch {
  *   weights[b][h'][j] += sum over the query heads h of h' of p_bhj, j < lens[b]
  * (0 for holes); other entries stay as they are.
  * Lengths are split over workgroups, and the parts joined in order of
- * position, in a second launch; short ones are not split. */
+ * position, in a second launch; short ones are not split.  Both, and the
+ * workspace, are sized for max_len and the current device; GEMV_E_UNSUPPORTED
+ * where a launch would pass 2^30 work-items (about 4 million parts of 1024
+ * slots). */
 size_t gemv_attention_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* batch, int q_heads, int weighted);
 
 int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const void* q, int64_t q_stride,
@@ -90,8 +93,8 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
  * With `weights` (float) and `positions` (int32), both [batch][heads][slots],
  * and seen (int32 [batch]: the tokens that the sequence has had in all, the
  * new ones included), a written slot also gets weight 0 and the token's
- * position, counted from 0: the state that gemv_kv_evict goes by.  All three
- * or none (GEMV_E_INVAL).
+ * position, counted from 0: the state that gemv_kv_evict goes by; a slot from
+ * `slots` on is written without them.  All three or none (GEMV_E_INVAL).
  * A page that is written must belong to one sequence of the call. */
 int gemv_kv_append(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* starts, const void* k,
                    int64_t k_stride, const void* v, int64_t v_stride, int rows, float* weights, int32_t* positions,

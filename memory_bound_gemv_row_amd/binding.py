@@ -514,7 +514,7 @@ def gemm_q8(A, scale, x, x_scale, out=None, out_dtype=None, stream=None):
     _dims(T, M, N)
     here = _here()
     a = _ptr(A, "A", torch.int8, (M, N), here)
-    s = _ptr(scale, "scale", torch.float16, (M,), here) if scale.dtype is torch.float16 else \
+    s = _ptr(scale, "scale", torch.float16, (M,), here) if getattr(scale, "dtype", None) is torch.float16 else \
         _need(scale, "scale", (torch.float16, torch.int16, torch.uint16), (M,))
     xp = _ptr(x, "x", torch.int8, (T, N), here)
     xs = _ptr(x_scale, "x_scale", torch.float32, (T,), here)

@@ -78,8 +78,8 @@ bool whole_tiles(const gemv_kv_cache* c) { return c->page_size % 16 == 0 && c->s
 // 28.9).  Others run at the card's bandwidth with one workgroup per CU, and a
 // second round that is mostly empty costs most: the least estimate, in slots,
 // of what the busiest CU reads, with 100 for a workgroup's start and end and
-// 150 for a join.  8 key-value heads of 128, 2 x 8192 slots: 18.3 us, with two
-// workgroups per CU 21.2, with four 24.0; 32 x 1024: 24.7, 31.1, 30.9; 5 heads of
+// 150 for a join.  8 key-value heads of 128, 2 x 8192 slots: 19 us, with two
+// workgroups per CU 21.2, with four 24.0; 32 x 1024: 25, 31.1, 30.9; 5 heads of
 // 96, 32 x 2000: three parts; one, two and four per CU 41.3, 34.8, 37.6.
 int chunk_for(int64_t items, int limit, int dim, int cus)
 {
@@ -222,7 +222,8 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
     const int64_t grid = cache->heads * (p.tiles > 1 ? (ranges + 7) / 8 * 8 * p.tiles : ranges);
     const int64_t joins = p.parts > 1 ? (int64_t)batch->batch * q_heads : 0;
     int blocks = weights != nullptr ? (int)(((int64_t)a.at.limit + 1023) / 1024) : 0;
-    if (!fits(grid, kLoneWaves * 64) || !fits(joins + items * blocks, 256))
+    const int block = (p.lone ? kLoneWaves : kWaves) * 64;
+    if (!fits(grid, block) || !fits(joins + items * blocks, 256))
         return GEMV_E_UNSUPPORTED;
     char* ws = static_cast<char*>(workspace);
     a.k = static_cast<const uint16_t*>(cache->k);
@@ -248,7 +249,6 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
     a.weights_wide = slots % 4 == 0 && aligned(weights, 16);
     void* args[] = {(void*)&a};
     const void* fn = cache->dtype == GEMV_F16 ? attention_for<kF16>(cache, p.lone) : attention_for<kBF16>(cache, p.lone);
-    const int block = (p.lone ? kLoneWaves : kWaves) * 64;
     if (int rc = launch(fn, grid, block, args, stream); rc != GEMV_OK)
         return rc;
     if (joins + items * blocks == 0)
@@ -342,9 +342,11 @@ int gemv_kv_evict(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const 
     const int64_t items = (int64_t)batch->batch * cache->heads;
     // two pieces a thread; a move has head_dim / 4 of them
     int blocks = (int)(((int64_t)a.moves_max * (cache->head_dim / 4) + 511) / 512);
-    blocks = blocks > 1024 ? 1024 : blocks;
-    if (!fits(items, kEvictThreads) || !fits(items * blocks, 256))
+    if (!fits(items, kEvictThreads))
         return GEMV_E_UNSUPPORTED;
+    const int64_t most = gemv_device::kMaxWorkItems / 256 / items;   // at least 4; the blocks walk what lies beyond
+    blocks = blocks > 1024 ? 1024 : blocks;
+    blocks = blocks > most ? (int)most : blocks;
     a.k = static_cast<uint16_t*>(cache->k);
     a.v = static_cast<uint16_t*>(cache->v);
     a.seen = seen;

@@ -573,6 +573,8 @@ append_kernel(Append a)
         if (slot < 0 || slot >= a.at.limit)
             continue;
         const int64_t to = a.at.offset(b, (int)slot);
+        if (to < 0)
+            continue;
         if (a.weights != nullptr) {
             for (int h = lane; h < a.heads; h += 64) {
                 if (slot < a.slots) {
@@ -582,8 +584,6 @@ append_kernel(Append a)
                 }
             }
         }
-        if (to < 0)
-            continue;
         const int per_head = a.dim >> 3, chunks = a.heads * per_head;
         for (int c = lane; c < chunks; c += 64) {
             const int h = c / per_head, d = (c - h * per_head) * 8;

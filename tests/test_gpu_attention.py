@@ -616,3 +616,48 @@ print("first-call capture ok", flush=True)
     say("[serving graph] first call captured, fresh process")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
     assert r.returncode == 0 and "first-call capture ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+def test_append_tracks_only_what_it_writes(gpu):
+    # a token in a hole leaves weights and positions as they were; one past the
+    # tracked slots is written without them
+    pool = ref.Pool([20, 30], 2, 64, 16, seed=1, width=2)
+    pool.table[0, 1] = -1
+    pool.dtable = pool.table.cuda()
+    g = torch.Generator().manual_seed(1)
+    new = torch.randn((2, 2, 64), generator=g).to(torch.float16)
+    want_k, _ = _append_reference(pool, [20, 30], [1, 1], new, new)
+    w = torch.full((2, 2, 24), 5.0, device="cuda")
+    pos = torch.full((2, 2, 24), 7, dtype=torch.int32, device="cuda")
+    say("[append] a hole and a slot past the tracked ones")
+    binding.kv_append(binding.PagedCache(pool.dk, pool.dv), pool.dtable, pool.dlens,
+                      torch.arange(3, dtype=torch.int32, device="cuda"), new.cuda(), new.cuda(), weights=w, positions=pos,
+                      seen=pool.dlens)
+    assert torch.all(w == 5) and torch.all(pos == 7) and _same(pool.dk.cpu(), want_k)
+
+
+def test_evict_of_many_sequences(gpu):
+    # more heads than the moving launch has blocks for at their usual number
+    B, H, n, budget, page = 3000, 2, 160, 70, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    width = n // page
+    k = torch.randn((B * width, page, H, 8), generator=g, device="cuda").half()
+    table = torch.randperm(B * width, generator=g, device="cuda").to(torch.int32).view(B, width)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    w = torch.rand((B, H, n), generator=g, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").expand(B, H, n).contiguous()
+    before = k.clone()
+    say("[evict] 6000 heads")
+    cache = binding.PagedCache(k, k.clone())
+    new_w, new_p, left = binding.kv_evict(cache, table, lens, lens, w, pos, budget, 5)
+    assert torch.all(left == budget) and torch.all(new_p[..., budget:] == -1)
+    kept = torch.where(pos >= n - 5, torch.inf, w).topk(budget, dim=2).indices.sort(2).values
+    assert torch.equal(new_p[..., :budget].sort(2).values.long(), kept)      # positions are slots here
+    assert torch.equal(new_w[..., :budget], w.gather(2, new_p[..., :budget].long()))
+    at = new_p[..., :budget].long()
+    b = torch.arange(B, device="cuda").view(B, 1, 1)
+    h = torch.arange(H, device="cuda").view(1, H, 1)
+    old = before[table.long()[b, at // page], at % page, h]
+    now = k[table.long()[b, torch.arange(budget, device="cuda").view(1, 1, -1) // page],
+            torch.arange(budget, device="cuda").view(1, 1, -1) % page, h]
+    assert torch.equal(old, now)
