@@ -706,9 +706,9 @@ __device__ __forceinline__ void move_row(const Evict& a, int b, int h, int from,
 // are matched with the evicted ones below it.
 //
 // Keys are made once and stay in LDS, up to kHeldKeys; those of longer
-// sequences are made anew in each pass, from cache.  (Held in registers, 32 a
-// lane, the unrolled code outgrew the instruction cache: 49 us for 4 x 8 heads
-// of 20000 to 32768 slots.)  A wave takes consecutive groups of 64 slots, one a
+// sequences are made anew in each pass, from cache.  (4 x 8 heads of 20000 to
+// 32768 slots: 36 to 42 us; with keys in registers, 32 a lane, 45 to 49.  32 x 8
+// heads of 2049 slots, one to go: 11 us.)  A wave takes consecutive groups of 64 slots, one a
 // lane, so the order of slots is that of (wave, group, lane), and counts before
 // a slot are population counts of lane masks and one sum over the waves.
 //
