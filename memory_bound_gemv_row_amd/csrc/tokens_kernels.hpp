@@ -531,7 +531,6 @@ store_tile(const i32x4 (&acc)[BT / WT / 16][BM / WM / 16], [[maybe_unused]] int*
                 }
         }
     } else {
-        wait_and_meet<0>();
         for (int i = threadIdx.x; i < BT * BM; i += kThreads)
             sums[i] = 0;
         __syncthreads();
@@ -656,6 +655,9 @@ gemm_q8_stream(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale,
         if constexpr (S > 6) { if (k0 + 6 * C >= N) break; stage(b6, b5, k0 + 6 * C); }
         if constexpr (S > 7) { if (k0 + 7 * C >= N) break; stage(b7, b6, k0 + 7 * C); }
     }
+    // no load may still be on its way to LDS that is reused below, or by the
+    // next workgroup
+    wait_and_meet<0>();
     store_tile<DT, BT, BM, WT, WM, WK>(acc, reinterpret_cast<int*>(b0), scale, x_scale, y, T, M, t0, m0);
 }
 
