@@ -661,3 +661,11 @@ def test_evict_of_many_sequences(gpu):
     now = k[table.long()[b, torch.arange(budget, device="cuda").view(1, 1, -1) // page],
             torch.arange(budget, device="cuda").view(1, 1, -1) % page, h]
     assert torch.equal(old, now)
+
+
+def test_more_query_heads_than_a_join_holds(gpu):
+    # the weights of 70 and 130 query heads over one key-value head, short and split
+    for heads in (70, 130):
+        _check(ref.Pool([300, 40], 1, 64, 16, seed=heads), _query(2, heads, 64, torch.float16, heads), f"{heads} over 1")
+        _check(ref.Pool([1300, 7], 1, 128, 16, torch.bfloat16, seed=heads), _query(2, heads, 128, torch.bfloat16, heads),
+               f"{heads} over 1, split")
