@@ -149,3 +149,65 @@ def evict(lens, seen, weights, positions, budget, recent, slots):
                 w_out[b, h, j] = weights[b, h, source[b, h, j]]
                 p_out[b, h, j] = positions[b, h, source[b, h, j]]
     return source, w_out, p_out, left
+
+
+# ---------------------------------------------------------------- bounds slot by slot
+def gathered(pool, t, b, n):
+    """Rows of the first n slots of sequence b, float64 [heads, n, dim], and which are held."""
+    j = np.arange(n)
+    page = pool.table.numpy()[b, j // pool.page].astype(np.int64)
+    held = (page >= 0) & (page < t.shape[0])
+    rows = t[torch.from_numpy(np.where(held, page, 0)), torch.from_numpy(j % pool.page)].double().numpy()
+    return np.where(held[:, None, None], rows, 0).transpose(1, 0, 2), held
+
+
+def attention_by_slot(pool, q, scale):
+    """As `attention`, with the error of every slot's power weighed by its own
+    probability, so that a token without weight adds nothing to the bound.
+
+    With x the logits, e_j = 2 D u |k_j| . |q| scale + 6 u (|x_j| + |max x|) is
+    the absolute error of x_j - reference (see `attention`; what the reference's
+    rises multiply by is counted here too, for their differences add up to at
+    most that between the first and the last).  A power is then off by at most
+    exp(x_j + e_j) - exp(x_j), by exp2's two units in the last place (4 u) and,
+    below 2^-126, by itself.  A wave's sums run over at most a quarter of the
+    length in tiles of 16, each with 16 additions and at most one rescaling (an
+    exp2 and a product, 5 u; 24 holds them), then 8 waves and len / 64 + 1 parts.
+    The normaliser's error S is the sum of those of the powers; a probability's
+    is (its own + p S) / (1 - S).  A logit of -inf has probability 0."""
+    B, Hq, D = q.shape
+    H, G = pool.heads, Hq // pool.heads
+    slots = pool.width * pool.page
+    out, bound = np.zeros((B, Hq, D)), np.zeros((B, Hq, D))
+    weights, wbound = np.zeros((B, H, slots)), np.zeros((B, H, slots))
+    for b, n in enumerate(pool.lens):
+        n = max(0, min(n, slots))
+        if n == 0:
+            continue
+        k, held = gathered(pool, pool.k, b, n)
+        v, _ = gathered(pool, pool.v, b, n)
+        qd = q[b].double().numpy().reshape(H, G, D)
+        with np.errstate(invalid="ignore"):
+            x = np.where(held, (qd @ k.transpose(0, 2, 1)) * scale, -np.inf)
+        counts = x > -np.inf
+        if not counts.any():
+            continue
+        top = x.max(-1, keepdims=True)
+        k = np.where(np.isfinite(k), k, 0)
+        mag = (np.abs(qd) @ np.abs(k).transpose(0, 2, 1)) * abs(scale)
+        far = np.where(counts, x, 0)
+        e = np.where(counts, 2 * D * U32 * mag + 6 * U32 * (np.abs(far) + np.abs(top)), 0)
+        power = np.exp(x - top)
+        Z = power.sum(-1, keepdims=True)
+        p = power / Z
+        sums = (24 * -(-n // 64) + 8 + n // 64 + 1) * U32
+        diff = (np.exp(x - top + e) - power) / Z + p * (4 * U32 + sums) + np.where(counts, 2.0 ** -126, 0)
+        S = diff.sum(-1, keepdims=True)
+        assert np.all(S < 0.5), "logits too large for this bound"
+        off = (diff + p * S) / (1 - S)
+        out[b] = (p @ v).reshape(Hq, D)
+        bound[b] = ((off + 2 * U32 * p) @ np.abs(v)).reshape(Hq, D)
+        weights[b, :, :n] = p.sum(1)
+        wbound[b, :, :n] = (off + (G + 2) * U32 * p).sum(1)
+    half = HALF_STEP[q.dtype]
+    return out, bound * (1 + half) + half * np.abs(out) + SMALLEST[q.dtype], weights, wbound

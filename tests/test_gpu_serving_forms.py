@@ -1,5 +1,7 @@
 """Every kernel that the serving operators' launch rules can choose, against
-plain 64-bit forms: the product at each of its tilings."""
+plain 64-bit forms: the product at each of its tilings, and attention over
+whole and loose pages at each head size, in one part, by one workgroup of
+eight waves, and split."""
 import numpy as np
 import pytest
 import torch
@@ -59,3 +61,48 @@ def test_products_of_whole_columns_in_unaligned_rows(gpu, T, M, N):
 def test_products_of_large_tiles(gpu, T, M, N):
     assert rules.product_kernel(T, M, N, _cus())[0] == "tiles"
     _check_products(T, M, N, T + M)
+
+
+# ---------------------------------------------------------------- attention
+def _check_attention(pool, q, label, scale=None):
+    say(f"[attention] {label}")
+    scale = pool.dim ** -0.5 if scale is None else scale
+    want, bound, want_w, wbound = ref.attention_by_slot(pool, q, scale)
+    cache = binding.PagedCache(pool.dk, pool.dv)
+    out = binding.paged_attention(cache, pool.dtable, pool.dlens, q.cuda(), scale=scale)
+    off = np.abs(out.cpu().double().numpy() - want)
+    assert np.all(off <= bound), (label, float(np.nanmax(off / bound)), int(np.isnan(off).sum()))
+    before = np.random.default_rng(1).uniform(0, 2, want_w.shape).astype(np.float32)
+    w = torch.from_numpy(before.copy()).cuda()
+    again = binding.paged_attention(cache, pool.dtable, pool.dlens, q.cuda(), scale=scale, weights=w)
+    assert torch.equal(again, out), label
+    got = w.cpu().double().numpy()
+    assert np.all(np.abs(got - (before + want_w)) <= wbound + ref.U32 * (before + want_w)), label
+    for b, n in enumerate(pool.lens):
+        assert np.array_equal(got[b, :, n:], before[b, :, n:]), label
+
+
+def _query(B, heads, dim, dtype, seed):
+    return torch.randn((B, heads, dim), generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:], ids=str)
+@pytest.mark.parametrize("dim", rules.DIMS)
+@pytest.mark.parametrize("page", rules.PAGES)
+@pytest.mark.parametrize("name", list(rules.LENGTHS))
+def test_attention_in_every_form(gpu, name, page, dim, dtype):
+    lens, kv, heads = rules.LENGTHS[name]
+    pool = ref.Pool(lens, kv, dim, page, dtype, seed=dim + page)
+    _check_attention(pool, _query(len(lens), heads, dim, dtype, page), f"{name}: dim {dim} page {page} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:], ids=str)
+@pytest.mark.parametrize("page,n", [(16, 64), (5, 64), (16, 1500)])
+def test_masked_keys_weigh_nothing(gpu, page, n, dtype):
+    # tokens masked by the lowest finite key, and one by a key of -inf
+    pool = ref.Pool([n], 1, 64, page, dtype, seed=12)
+    for j in (0, 5, 40, n - 1):
+        pool.k[pool.table[0, j // page], j % page, 0] = -65504.0
+    pool.k[pool.table[0, 19 // page], 19 % page] = -float("inf")
+    pool.dk = pool.k.cuda()
+    _check_attention(pool, torch.ones((1, 2, 64), dtype=dtype), f"masked keys, {n} in pages of {page} {dtype}", scale=0.125)

@@ -1,7 +1,17 @@
-"""That the shapes of the GPU tests reach every kernel of the serving operators."""
+"""That the shapes of the GPU tests reach every kernel of the serving
+operators, and that the bounds they are held to catch mistakes."""
+import numpy as np
+import pytest
+import torch
+
+import serving_ref as ref
 import serving_rules as rules
 
 CUS = 256
+
+
+def _limit(lens, page):
+    return max(-(-n // page) for n in lens) * page
 
 
 def test_every_tiling_of_the_product_is_reached():
@@ -27,3 +37,44 @@ def test_large_tiles_are_reached_whole_and_halved():
     assert forms == {(True, False), (False, True), (False, False)}
     # of the halved ones, one ends in the first half of its last tile
     assert any(0 < M % 256 <= 128 and -(-T // 256) * -(-M // 256) > CUS for T, M, _ in rules.LARGE)
+
+
+def test_every_form_of_the_attention_is_reached():
+    forms = set()
+    for dim in rules.DIMS:
+        for page in rules.PAGES:
+            for lens, kv, heads in rules.LENGTHS.values():
+                dp, whole, lone, parts = rules.attention_form(len(lens), _limit(lens, page), kv, heads, dim, page, CUS)
+                forms.add((dp, whole, whole and dim == dp, lone, parts > 1))
+    for dp in (64, 128, 256):
+        for split in (False, True):
+            assert (dp, False, False, False, split) in forms, (dp, split)
+        for exact in (False, True):
+            assert (dp, True, exact, True, False) in forms
+            for split in (False, True):
+                assert (dp, True, exact, False, split) in forms, (dp, exact, split)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+def test_the_bound_catches_attention_to_masked_tokens(dtype):
+    # keys of the lowest value: their logits' large error must not widen the bound
+    pool = ref.Pool([64], 1, 64, 16, dtype, seed=12, device="cpu")
+    for j in (0, 5, 40):
+        pool.k[pool.table[0, j // 16], j % 16, 0] = -65504.0
+    pool.k[pool.table[0, 1], 3] = -float("inf")
+    q = torch.ones((1, 2, 64), dtype=dtype)
+    out, bound, w, wbound = ref.attention_by_slot(pool, q, 0.125)
+    assert np.all(w[0, 0, [0, 5, 19, 40]] == 0) and np.all(np.isfinite(bound)) and np.all(wbound < 1e-3)
+    v = ref.gathered(pool, pool.v, 0, 64)[0][0]
+    for wrong in (v.mean(0), np.zeros(64), v[[0, 5, 40]].mean(0), v[1], 1.02 * out[0, 0]):
+        assert np.any(np.abs(wrong - out[0, 0]) > bound[0, 0])
+
+
+def test_the_bounds_agree_where_both_apply():
+    pool = ref.Pool([130, 0, 33], 2, 80, 5, torch.float16, seed=3, device="cpu")
+    pool.table[0, 2] = -1
+    q = torch.randn((3, 6, 80), generator=torch.Generator().manual_seed(1)).half()
+    for a, b in zip(ref.attention(pool, q, 0.1)[::2], ref.attention_by_slot(pool, q, 0.1)[::2]):
+        assert np.allclose(a, b, rtol=1e-12, atol=1e-15)
+    wide, narrow = ref.attention(pool, q, 0.1)[1], ref.attention_by_slot(pool, q, 0.1)[1]
+    assert np.all(narrow <= 2 * wide) and np.all(narrow > 0)
