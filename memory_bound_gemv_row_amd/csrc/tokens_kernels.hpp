@@ -570,7 +570,8 @@ gemm_q8_stream(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale,
     constexpr int FT = BT / WT / 16, FM = BM / WM / 16;
     constexpr int kRow = C / 16;                          // pieces of a row
     constexpr int kPieces = (BT + BM) * kRow, L = kPieces / kThreads;
-    static_assert(kPieces % kThreads == 0 && kThreads % kRow == 0 && S <= 8, "whole rounds of loads");
+    static_assert(kPieces % kThreads == 0 && kThreads % kRow == 0, "whole rounds of loads");
+    static_assert(S >= 3 && S <= 5, "stages that there are buffers for");
     static_assert((kThreads / kRow) % 16 == 0, "the swizzle repeats over the rounds of loads");
     static_assert(BT % (kThreads / kRow) == 0, "a round loads rows of one operand");
     static_assert(WK == 1 || BT * BM * 4 <= kPieces * 16, "the sums fit one buffer");
@@ -578,12 +579,9 @@ gemm_q8_stream(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale,
     // a buffer each, so that the compiler knows which of them a load fills
     __shared__ i32x4 b0[kPieces];
     __shared__ i32x4 b1[kPieces];
-    __shared__ i32x4 b2[S > 2 ? kPieces : 1];
+    __shared__ i32x4 b2[kPieces];
     __shared__ i32x4 b3[S > 3 ? kPieces : 1];
     __shared__ i32x4 b4[S > 4 ? kPieces : 1];
-    __shared__ i32x4 b5[S > 5 ? kPieces : 1];
-    __shared__ i32x4 b6[S > 6 ? kPieces : 1];
-    __shared__ i32x4 b7[S > 7 ? kPieces : 1];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wk = wave % WK, wm = wave / WK % WM, wt = wave / WK / WM;
@@ -637,23 +635,18 @@ gemm_q8_stream(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale,
         multiply(now);
     };
     fetch(b0, 0);
-    if constexpr (S > 2) fetch(b1, C);
+    fetch(b1, C);
     if constexpr (S > 3) fetch(b2, 2 * C);
     if constexpr (S > 4) fetch(b3, 3 * C);
-    if constexpr (S > 5) fetch(b4, 4 * C);
-    if constexpr (S > 6) fetch(b5, 5 * C);
-    if constexpr (S > 7) fetch(b6, 6 * C);
-    i32x4* const last = S == 2 ? b1 : S == 3 ? b2 : S == 4 ? b3 : S == 5 ? b4 : S == 6 ? b5 : S == 7 ? b6 : b7;
+    i32x4* const last = S == 3 ? b2 : S == 4 ? b3 : b4;
     for (int k0 = 0; k0 < N; k0 += S * C) {
         stage(b0, last, k0);
         if (k0 + C >= N) break;
         stage(b1, b0, k0 + C);
-        if constexpr (S > 2) { if (k0 + 2 * C >= N) break; stage(b2, b1, k0 + 2 * C); }
+        if (k0 + 2 * C >= N) break;
+        stage(b2, b1, k0 + 2 * C);
         if constexpr (S > 3) { if (k0 + 3 * C >= N) break; stage(b3, b2, k0 + 3 * C); }
         if constexpr (S > 4) { if (k0 + 4 * C >= N) break; stage(b4, b3, k0 + 4 * C); }
-        if constexpr (S > 5) { if (k0 + 5 * C >= N) break; stage(b5, b4, k0 + 5 * C); }
-        if constexpr (S > 6) { if (k0 + 6 * C >= N) break; stage(b6, b5, k0 + 6 * C); }
-        if constexpr (S > 7) { if (k0 + 7 * C >= N) break; stage(b7, b6, k0 + 7 * C); }
     }
     // no load may still be on its way to LDS that is reused below, or by the
     // next workgroup
