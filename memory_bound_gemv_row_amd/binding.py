@@ -464,6 +464,15 @@ def _rows(t, name, dtype, shape, device, dense):
     return t.data_ptr(), t.stride(0)
 
 
+def _apart(outs, ins):
+    """Refuses outputs that share memory with each other or with inputs, each
+    given as (address, bytes)."""
+    for i, (p, n) in enumerate(outs):
+        for q, m in outs[i + 1:] + ins:
+            if n and m and p < q + m and q < p + n:
+                raise ValueError("the outputs must not overlap the inputs or each other")
+
+
 _codes = {}
 
 
@@ -699,8 +708,9 @@ def kv_evict(cache, table, lens, seen, weights, positions, budget, recent, max_l
         new_w, new_p, left = out
         outs = (_ptr(new_w, "out[0]", torch.float32, shape, here), _ptr(new_p, "out[1]", torch.int32, shape, here),
                 _ptr(left, "out[2]", torch.int32, (B,), here))
-        if weights.numel() and (outs[0] == wp or outs[1] == pp) or B and outs[2] == batch.lens:
-            raise ValueError("the outputs must not be the inputs")
+        tracked = 4 * weights.numel()
+        _apart([(outs[0], tracked), (outs[1], tracked), (outs[2], 4 * B)],
+               [(wp, tracked), (pp, tracked), (batch.lens, 4 * B), (np, 4 * B)])
     lib, c, s = load(), cache._by_ref, ctypes.byref(batch)
     need = cache._need((B, budget, room), lambda: lib.gemv_kv_evict_workspace(c, s, budget))
     work = empty(need, dtype=torch.uint8, device=cache.device) if need else None

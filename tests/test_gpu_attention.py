@@ -669,3 +669,20 @@ def test_more_query_heads_than_a_join_holds(gpu):
         _check(ref.Pool([300, 40], 1, 64, 16, seed=heads), _query(2, heads, 64, torch.float16, heads), f"{heads} over 1")
         _check(ref.Pool([1300, 7], 1, 128, 16, torch.bfloat16, seed=heads), _query(2, heads, 128, torch.bfloat16, heads),
                f"{heads} over 1, split")
+
+
+def test_evict_refuses_outputs_that_overlap(gpu):
+    # in part, with one another, and `seen`, which workgroups read while another writes the lengths
+    pool = ref.Pool([20, 20], 2, 64, 16, seed=1)
+    cache = binding.PagedCache(pool.dk, pool.dv)
+    w = torch.rand((3, 2, 2, 32), device="cuda")
+    pos = torch.zeros((3, 2, 2, 32), dtype=torch.int32, device="cuda")
+    seen, left = pool.dlens.clone(), torch.zeros(2, dtype=torch.int32, device="cuda")
+    part = w.flatten()[64: 192].view(2, 2, 32)              # the second half of w[0] and the first of w[1]
+    say("[evict] outputs that overlap")
+    for out in ((part, pos[1], left), (w[1], pos[0], left), (w[1], pos[1], pool.dlens), (w[1], pos[1], seen),
+                (w[1], w[1].view(torch.int32), left), (w[1], pos[1], pos[1, 0, 0, :2])):
+        with pytest.raises(ValueError):
+            binding.kv_evict(cache, pool.dtable, pool.dlens, seen, w[0], pos[0], 8, 2, out=out)
+    binding.kv_evict(cache, pool.dtable, pool.dlens, seen, w[0], pos[0], 8, 2, out=(w[1], pos[1], left))
+    assert torch.all(left == 8)

@@ -180,3 +180,13 @@ def test_package_exports_the_operators():
     for name in ("quantize_tokens_q8", "gemm_q8", "PagedCache", "paged_attention", "kv_append", "kv_evict"):
         assert getattr(amd, name) is getattr(binding, name)
     assert os.path.exists(os.path.join(build.INCLUDE, "gemv_attention.h"))
+
+
+def test_outputs_that_share_memory_are_refused():
+    apart = binding._apart
+    apart([(100, 40), (140, 40), (180, 4)], [(0, 100), (200, 40), (184, 4)])
+    apart([(100, 0), (100, 40)], [(100, 0)])              # nothing shares nothing
+    for outs, ins in (([(100, 40)], [(100, 40)]), ([(100, 40)], [(139, 1)]), ([(100, 40)], [(0, 101)]),
+                      ([(100, 40)], [(110, 2)]), ([(100, 40), (120, 40)], []), ([(0, 4), (8, 4), (11, 4)], [])):
+        with pytest.raises(ValueError):
+            apart(outs, ins)
