@@ -65,7 +65,8 @@ typedef struct gemv_kv_batch {
  * query head h using key-value head h' = h / (q_heads / heads).
  *   q     [batch][q_heads][head_dim] of the cache's type, sequences q_stride
  *         elements apart (a multiple of 8); q_heads a multiple of heads;
- *   out   [batch][q_heads][head_dim] of the cache's type, dense.
+ *   out   [batch][q_heads][head_dim] of the cache's type, dense; it may be q
+ *         itself, where q is dense, and overlaps nothing else.
  * A sequence of length 0, with holes only, or with no logit above -inf gets
  * zeros.  Products are summed and the softmax is taken in binary32; the
  * probabilities are not rounded before they meet the values.
@@ -95,7 +96,8 @@ int gemv_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
  * new ones included), a written slot also gets weight 0 and the token's
  * position, counted from 0: the state that gemv_kv_evict goes by; a slot from
  * `slots` on is written without them.  All three or none (GEMV_E_INVAL).
- * A page that is written must belong to one sequence of the call. */
+ * A page that is written must belong to one sequence of the call and stand in
+ * its table once; k and v must not overlap the cache. */
 int gemv_kv_append(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* starts, const void* k,
                    int64_t k_stride, const void* v, int64_t v_stride, int rows, float* weights, int32_t* positions,
                    const int32_t* seen, int64_t slots, hipStream_t stream);
@@ -115,8 +117,11 @@ int gemv_kv_append(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
  * The outputs must not overlap the inputs.  Keys and values move in place;
  * slots from `budget` on keep their contents.  A kept token in a hole moves
  * nothing, and nothing moves into a hole.  Pages must belong to one sequence
- * of the call: copy a shared page before evicting from it.
- * 0 <= budget, 0 <= recent (GEMV_E_INVAL otherwise). */
+ * of the call, once: copy a shared page before evicting from it.
+ * 0 <= budget, 0 <= recent (GEMV_E_INVAL otherwise).  Keep recent <= budget:
+ * the newest tokens are equals, so where they alone are more than the budget
+ * those in the lower slots stay, which are not the latest of them.
+ * GEMV_E_UNSUPPORTED from 2^20 heads of sequences on (batch * heads). */
 size_t gemv_kv_evict_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* batch, int budget);
 
 int gemv_kv_evict(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* seen, const float* weights,

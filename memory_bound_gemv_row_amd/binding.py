@@ -622,7 +622,8 @@ def paged_attention(cache, table, lens, q, scale=None, max_len=None, weights=Non
     lens int32 [batch]; scale 1 / sqrt(head_dim) unless given; max_len the
     longest length, where the host knows one below the table's room.
     weights float32 [batch, heads, slots]: each token's attention weights,
-    summed over the query heads of its head, are added to it."""
+    summed over the query heads of its head, are added to it.  out may be a
+    dense q itself."""
     import torch
 
     here = _here()
@@ -684,8 +685,9 @@ def kv_append(cache, table, lens, starts, k, v, weights=None, positions=None, se
 def kv_evict(cache, table, lens, seen, weights, positions, budget, recent, max_len=None, out=None, stream=None):
     """Evicts from a paged cache by accumulated attention weight: each head of
     a sequence over `budget` keeps its tokens of the last `recent` positions
-    and of the others those of the largest weight, `budget` in all; keys and
-    values move in place.  weights float32 and positions int32 [batch, heads,
+    and of the others those of the largest weight, `budget` in all (keep
+    recent <= budget: of more newest tokens than that, those in the lower slots
+    stay, not the latest); keys and values move in place.  weights float32 and positions int32 [batch, heads,
     slots], seen int32 [batch] (see kv_append).  Returns, or writes to
     ``out``, (weights, positions, lens) afterwards."""
     import torch

@@ -686,3 +686,26 @@ def test_evict_refuses_outputs_that_overlap(gpu):
             binding.kv_evict(cache, pool.dtable, pool.dlens, seen, w[0], pos[0], 8, 2, out=out)
     binding.kv_evict(cache, pool.dtable, pool.dlens, seen, w[0], pos[0], 8, 2, out=(w[1], pos[1], left))
     assert torch.all(left == 8)
+
+
+@pytest.mark.parametrize("lens,kv,heads", [([60, 3], 2, 6), ([250, 17], 2, 40), ([1500, 700], 1, 34)])
+def test_attention_in_place(gpu, lens, kv, heads):
+    # the outputs in the queries' memory: one part, one workgroup of eight waves, split and joined
+    pool = ref.Pool(lens, kv, 64, 16, torch.bfloat16, seed=heads)
+    cache = binding.PagedCache(pool.dk, pool.dv)
+    q = _query(len(lens), heads, 64, torch.bfloat16, heads).cuda()
+    want = binding.paged_attention(cache, pool.dtable, pool.dlens, q)
+    w, again = (torch.zeros((len(lens), kv, pool.width * 16), device="cuda") for _ in range(2))
+    say(f"[attention] in place, {heads} heads over {kv}")
+    binding.paged_attention(cache, pool.dtable, pool.dlens, q.clone(), weights=w)
+    both = q.clone()
+    assert binding.paged_attention(cache, pool.dtable, pool.dlens, both, weights=again, out=both) is both
+    assert torch.equal(both, want) and torch.equal(w, again)
+
+
+def test_keys_and_values_of_one_buffer(gpu):
+    # the two as parts of one array, page by page, as many programs keep them
+    pool = ref.Pool([90, 1, 200], 2, 80, 16, torch.float16, seed=6)
+    both = torch.stack([pool.k, pool.v], 1).cuda()
+    pool.dk, pool.dv = both[:, 0], both[:, 1]
+    _check(pool, _query(3, 4, 80, torch.float16, 6), "keys and values in one buffer")
