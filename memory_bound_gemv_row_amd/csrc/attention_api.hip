@@ -72,20 +72,25 @@ struct Split {
 // Tiles of 16 slots that lie in one page, near enough for 32-bit offsets.
 bool whole_tiles(const gemv_kv_cache* c) { return c->page_size % 16 == 0 && c->stride_slot < (1 << 26); }
 
-// Slots of a part, a multiple of 64 (a tile for each wave) up to kMaxChunk.
-// Head sizes up to 64 have small tiles and wait for them: eight workgroups per
-// CU (16 heads of 64, 16 x 301 to 2047 slots: 24.5 us; with two 25.7, with one
-// 28.9).  Others run at the card's bandwidth with one workgroup per CU, and a
-// second round that is mostly empty costs most: the least estimate, in slots,
-// of what the busiest CU reads, with 100 for a workgroup's start and end and
-// 150 for a join.  8 key-value heads of 128, 2 x 8192 slots: 19 us, with two
-// workgroups per CU 21.2, with four 24.0; 32 x 1024: 25, 31.1, 30.9; 5 heads of
-// 96, 32 x 2000: three parts; one, two and four per CU 41.3, 34.8, 37.6.
+// Slots of a part, a multiple of 64 (a tile for each wave) up to kMaxChunk: the
+// least estimate, in slots, of what the busiest CU reads, with 100 for a
+// workgroup's start and end and 150 for a join.  A second round of workgroups
+// that is mostly empty costs most.  8 key-value heads of 128, 2 x 8192 slots:
+// 19 us, with two workgroups per CU 21.2, with four 24.0; 32 x 1024: 25, 31.1,
+// 30.9; 5 heads of 96, 32 x 2000: three parts; one, two and four per CU 41.3,
+// 34.8, 37.6.
+// Heads of up to 64 have small tiles and wait for them, so where the heads
+// alone fill the card and no part holds the whole length they are split into
+// eight workgroups per CU: 16 heads of 64, 16 x 301 to 2047 slots 23.8 us, by the
+// estimate 26.2; 8 heads, 64 x 100 to 1500 slots 29.8 and 37.3; 32 heads, 8 x 500
+// to 4000 slots 38.3 and 49.1.  Fewer heads, or lengths that one part holds, are
+// slower so: 4 heads, 1 x 30000 slots 39.9 and 15.5 by the estimate; 8 heads, 2 x
+// 8192 23.5 and 13.1; 32 x 1024 21.3 and 15.0.
 int chunk_for(int64_t items, int limit, int dim, int cus)
 {
-    if (dim <= 64) {
+    if (dim <= 64 && items >= cus && limit > kMaxChunk) {
         const int64_t chunk = ((int64_t)limit * items / ((int64_t)cus * 8) + 63) / 64 * 64;
-        return (int)(chunk < 64 ? 64 : (chunk > kMaxChunk ? kMaxChunk : chunk));
+        return (int)(chunk < kMaxChunk ? chunk : kMaxChunk);
     }
     int best = kMaxChunk;
     int64_t least = INT64_MAX;

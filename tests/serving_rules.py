@@ -50,8 +50,8 @@ def attention_form(batch, limit, kv_heads, q_heads, dim, page, cus=256):
     gemv_attention for slots near one another."""
     group = q_heads // kv_heads
     items = batch * kv_heads * -(-group // 16)
-    if dim <= 64:
-        chunk = min(max((limit * items // (cus * 8) + 63) // 64 * 64, 64), 1024)
+    if dim <= 64 and items >= cus and limit > 1024:
+        chunk = min((limit * items // (cus * 8) + 63) // 64 * 64, 1024)
     else:
         def cost(c):
             parts = -(-limit // c)

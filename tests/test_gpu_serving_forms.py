@@ -106,3 +106,22 @@ def test_masked_keys_weigh_nothing(gpu, page, n, dtype):
     pool.k[pool.table[0, 19 // page], 19 % page] = -float("inf")
     pool.dk = pool.k.cuda()
     _check_attention(pool, torch.ones((1, 2, 64), dtype=dtype), f"masked keys, {n} in pages of {page} {dtype}", scale=0.125)
+
+
+@pytest.mark.parametrize("dim", [8, 64, 72, 128, 256])
+def test_parts_are_those_of_the_rule(gpu, dim):
+    # the workspace holds a maximum, a sum and `dim` values of every query head and part
+    import ctypes
+
+    lib, cus = binding.load(), _cus()
+    for batch, limit, kv, heads in ((16, 2048, 16, 16), (64, 1504, 8, 8), (8, 4000, 32, 32), (1, 30000, 4, 16), (2, 8192, 8, 32),
+                                    (32, 1024, 8, 32), (8, 4000, 4, 28), (1, 250, 2, 4), (40, 500, 4, 4), (3, 77, 1, 50)):
+        for page in (16, 24):
+            k = torch.empty((1, page, kv, dim), dtype=torch.float16, device="cuda")
+            cache = binding.PagedCache(k, k)
+            width = -(-limit // page)
+            call = binding.KvBatch(cache.c.k, width, width, cache.c.k, batch, limit)
+            got = lib.gemv_attention_workspace(ctypes.byref(cache.c), ctypes.byref(call), heads, 0)
+            _, _, _, parts = rules.attention_form(batch, limit, kv, heads, dim, page, cus)
+            want = 0 if parts == 1 else -(-batch * heads * parts * 8 // 16) * 16 + batch * heads * parts * dim * 4
+            assert got == want, (batch, limit, kv, heads, page)

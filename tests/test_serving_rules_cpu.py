@@ -78,3 +78,17 @@ def test_the_bounds_agree_where_both_apply():
         assert np.allclose(a, b, rtol=1e-12, atol=1e-15)
     wide, narrow = ref.attention(pool, q, 0.1)[1], ref.attention_by_slot(pool, q, 0.1)[1]
     assert np.all(narrow <= 2 * wide) and np.all(narrow > 0)
+
+
+# parts of the length for heads of 64, with what the other rule took: one that
+# aims at eight workgroups per CU, or the estimate of what the busiest CU reads
+@pytest.mark.parametrize("batch,limit,kv,heads,parts", [
+    (16, 2048, 16, 16, 8),      # 23.8 us, by the estimate (2 parts) 26.2
+    (64, 1504, 8, 8, 4),        # 29.8 us, by the estimate 37.3
+    (8, 4000, 32, 32, 8),       # 38.3 us, by the estimate 49.1
+    (1, 30000, 4, 16, 59),      # 15.5 us, by workgroups per CU (469 parts) 39.9
+    (2, 8192, 8, 32, 16),       # 13.1 us, by workgroups per CU (128 parts) 23.5
+    (32, 1024, 8, 32, 1),       # 15.0 us, by workgroups per CU (8 parts) 21.3
+    (8, 4000, 4, 28, 8)])       # 13.6 us, by workgroups per CU (63 parts) 22.1
+def test_parts_of_small_heads(batch, limit, kv, heads, parts):
+    assert rules.attention_form(batch, limit, kv, heads, 64, 16, CUS)[2:] == (False, parts)
