@@ -709,3 +709,18 @@ def test_keys_and_values_of_one_buffer(gpu):
     both = torch.stack([pool.k, pool.v], 1).cuda()
     pool.dk, pool.dv = both[:, 0], both[:, 1]
     _check(pool, _query(3, 4, 80, torch.float16, 6), "keys and values in one buffer")
+
+
+def test_pages_shared_by_sequences(gpu):
+    # a common first part: one page in two tables, and twice in one; only unshared pages are written
+    pool = ref.Pool([70, 61, 40], 2, 64, 16, torch.bfloat16, seed=13)
+    pool.table[1, 0] = pool.table[0, 0]
+    pool.table[2, 1] = pool.table[2, 0]
+    pool.dtable = pool.table.cuda()
+    q = _query(3, 4, 64, torch.bfloat16, 13)
+    _check(pool, q, "shared pages")
+    new = torch.randn((3, 2, 64), generator=torch.Generator().manual_seed(13)).to(torch.bfloat16)
+    want_k, want_v = _append_reference(pool, pool.lens, [1, 1, 1], new, new)
+    binding.kv_append(binding.PagedCache(pool.dk, pool.dv), pool.dtable, pool.dlens,
+                      torch.arange(4, dtype=torch.int32, device="cuda"), new.cuda(), new.cuda())
+    assert _same(pool.dk.cpu(), want_k) and _same(pool.dv.cpu(), want_v)
