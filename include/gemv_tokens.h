@@ -46,8 +46,8 @@ int gemv_quantize_tokens_q8(const void* x, int dtype, int64_t stride, int8_t* q,
  * the output's type.  Every int8 value is accepted on both sides; N is at most
  * 131071, where no sum can leave 32 bits (GEMV_E_UNSUPPORTED beyond).
  * N == 0 writes products of zero.  M == 0 or T == 0 is a no-op.
- * GEMV_E_UNSUPPORTED too where a launch would pass 2^30 work-items (from about
- * 2^39 products y on); GEMV_E_INVAL for negative sizes, an unknown dtype or a
+ * GEMV_E_UNSUPPORTED too where a launch would pass 2^30 work-items (never below
+ * 2^25 elements of y); GEMV_E_INVAL for negative sizes, an unknown dtype or a
  * missing pointer.
  * The bandwidth path needs 16-byte-aligned A and x and N % 16 == 0; others
  * take a slower path, whose operands go through registers. */
