@@ -8,7 +8,8 @@
 // rows.  Reached on one MI355X, where a pure read makes 7.1 TB/s and a copy
 // 4.95 TB/s of reads and writes: attention 5.2 TB/s over 64 sequences of 100
 // to 8192 slots (8 heads of 128, 222 us; 6.0 TB/s where all have 8192), append
-// 5.2 TB/s (4 x 8191 tokens, 52 us).
+// 5.1 to 5.2 TB/s (4 x 8191 tokens, 52 us).  The same 64 sequences with other
+// heads: 8 of 64 127 to 132 us, 80 and 96 195 to 201, 256 460 us (5.1 TB/s).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -162,7 +163,9 @@ __device__ __forceinline__ Buffer buffer(const uint16_t* p, unsigned bytes)
 // A wave loads its next tile while it multiplies the current one.  Where
 // pages are whole numbers of tiles (WHOLE), a tile has one page and its
 // address is the same for all lanes; otherwise each row has an address of its
-// own.  EXACT: the head's size is DP, so no lane is without an element.
+// own, and its loads wait at a branch (64 sequences of 100 to 8192 slots in pages
+// of 5, 8 or 24: 266 to 269 us, where pages of 16 take 223; heads of 256, 659
+// against 460).  EXACT: the head's size is DP, so no lane is without an element.
 template <int DT, int DP, bool WHOLE, bool EXACT, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, DP == 256 ? 1 : 2)
 attention_kernel(Attention a)
@@ -708,7 +711,8 @@ __device__ __forceinline__ void move_row(const Evict& a, int b, int h, int from,
 // Keys are made once and stay in LDS, up to kHeldKeys; those of longer
 // sequences are made anew in each pass, from cache.  (4 x 8 heads of 20000 to
 // 32768 slots: 36 to 42 us; with keys in registers, 32 a lane, 45 to 49.  32 x 8
-// heads of 2049 slots, one to go: 11 us.)  A wave takes consecutive groups of 64 slots, one a
+// heads of 2049 slots, one to go: 11 us.  4 x 8 heads of 70000 to 131072 slots, past
+// kHeldKeys, and their moves: 376 us.)  A wave takes consecutive groups of 64 slots, one a
 // lane, so the order of slots is that of (wave, group, lane), and counts before
 // a slot are population counts of lane masks and one sum over the waves.
 //
@@ -970,7 +974,7 @@ evict_select_kernel(Evict a)
 }
 
 // What the selection leaves to do (4 x 8 heads, 110 MB of rows in pieces of
-// 256 bytes anywhere in the pool: 41 us): a thread per slot for the weights and
+// 256 bytes anywhere in the pool: 39 us): a thread per slot for the weights and
 // positions, then a thread per 16 bytes of the rows that move.
 __global__ void __launch_bounds__(256)
 evict_move_kernel(Evict a, int blocks)

@@ -6,10 +6,11 @@
 //
 // Up to some hundred tokens the product is bound by reading A, beyond by the
 // matrix units, which this card feeds at a clock that falls with their load
-// (1.55 GHz at 8192 x 8192 x 8192, the matrix units busy 64 % of it).  Reached
-// (tokens x outputs x inner): 1 x 4096 x 4096 4.7 us; 24 x 14336 x 4096 11.2 us,
-// 5.3 TB/s; 777 x 4096 x 14336 58 us, 1570 TOP/s; 4096 x 4096 x 14336 212 us,
-// 2270 TOP/s.
+// (1.45 to 1.55 GHz at 8192 x 8192 x 8192, by the card; the matrix units busy
+// 64 % of it).  Reached back to back in a captured graph (tokens x outputs x
+// inner): 1 x 4096 x 4096 5.1 us; 24 x 14336 x 4096 11.7 us, 5.1 TB/s; 777 x 4096 x
+// 14336 60 us, 1535 TOP/s (65 to 69 under a kernel trace); 4096 x 14336 x 4096 240
+// us, 2000 TOP/s; 4096 x 4096 x 14336 212 to 226 us, 2130 to 2270 TOP/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -174,8 +175,8 @@ struct Eight {   // eight consecutive elements as loaded
 };
 
 // Bound by memory (8192 x 8192 of binary16: 37 us, 5.4 TB/s read and written;
-// 777 x 14336 of binary32: 11.0 us, 5.05 TB/s), a single row by latency (4096 of
-// binary16: 2.9 us).
+// 777 x 14336 of binary32: 11.2 us, 5.0 TB/s, 13 under a kernel trace), a single
+// row by latency (4096 of binary16: 2.6 us).
 // Preconditions (host): N % 8 == 0, N >= 8, rows of x 16-byte aligned, rows
 // of q 8-byte aligned.  A workgroup of W waves owns a row and walks the grid;
 // rows of up to W * CH * 512 elements stay in registers between the maximum
@@ -242,7 +243,8 @@ quantize_tokens_kernel(const void* __restrict__ x, int64_t stride, int8_t* __res
     }
 }
 
-// Any N and alignment: a workgroup per row, element by element.
+// Any N and alignment: a workgroup per row, element by element, read twice
+// (8192 x 8191 of binary16: 123 us; 777 x 14335 of binary32: 40; a row of 4095: 6.0).
 template <int DT>
 __global__ void __launch_bounds__(256)
 quantize_tokens_elementwise(const void* __restrict__ x, int64_t stride, int8_t* __restrict__ q,
@@ -656,9 +658,9 @@ gemm_q8_stream(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale,
 
 // Any size and alignment.  The same tiles, but rows of any alignment come
 // through registers, two stages of C columns ahead, and are written to one of
-// two buffers; columns past N are zeros there.  1 x 4096 x 4095: 8.2 us;
-// 4096 x 4096 x 4095: 164 us, where the large tiles take 70 for 4096 columns:
-// pieces of any alignment cannot go straight to LDS.
+// two buffers; columns past N are zeros there.  1 x 4096 x 4095: 8.4 us; 777 x
+// 4096 x 14335: 114 us; 4096 x 4096 x 4095: 163 us, where the large tiles take 70 to
+// 77 for 4096 columns: pieces of any alignment cannot go straight to LDS.
 template <int DT, int BT, int BM, int WT, int WM, int WK, int C>
 __global__ void __launch_bounds__(WT * WM * WK * 64)
 gemm_q8_any(const int8_t* __restrict__ A, const uint16_t* __restrict__ scale, const int8_t* __restrict__ x,
