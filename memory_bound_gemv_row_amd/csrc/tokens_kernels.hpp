@@ -7,10 +7,11 @@
 // Up to some hundred tokens the product is bound by reading A, beyond by the
 // matrix units, which this card feeds at a clock that falls with their load
 // (1.45 to 1.55 GHz at 8192 x 8192 x 8192, by the card; the matrix units busy
-// 64 % of it).  Reached back to back in a captured graph (tokens x outputs x
-// inner): 1 x 4096 x 4096 5.1 us; 24 x 14336 x 4096 11.7 us, 5.1 TB/s; 777 x 4096 x
-// 14336 60 us, 1535 TOP/s (65 to 69 under a kernel trace); 4096 x 14336 x 4096 240
-// us, 2000 TOP/s; 4096 x 4096 x 14336 212 to 226 us, 2130 to 2270 TOP/s.
+// 64 % of it).  Reached back to back in a captured graph, where two figures
+// stand on two cards (tokens x outputs x inner): 1 x 4096 x 4096 5.1 us; 24 x 14336
+// x 4096 11.7 us, 5.1 TB/s; 777 x 4096 x 14336 60 and 66 us, 1535 and 1380 TOP/s;
+// 4096 x 14336 x 4096 240 and 259 us, 2000 and 1860 TOP/s; 4096 x 4096 x 14336 212
+// and 226 us, 2270 and 2130 TOP/s.
 #pragma once
 
 #include <hip/hip_runtime.h>
