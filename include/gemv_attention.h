@@ -121,7 +121,7 @@ int gemv_kv_append(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const
  * 0 <= budget, 0 <= recent (GEMV_E_INVAL otherwise).  Keep recent <= budget:
  * the newest tokens are equals, so where they alone are more than the budget
  * those in the lower slots stay, which are not the latest of them.
- * GEMV_E_UNSUPPORTED from 2^20 heads of sequences on (batch * heads). */
+ * GEMV_E_UNSUPPORTED beyond 2^20 heads of sequences (batch * heads). */
 size_t gemv_kv_evict_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* batch, int budget);
 
 int gemv_kv_evict(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* seen, const float* weights,

@@ -687,9 +687,9 @@ def kv_evict(cache, table, lens, seen, weights, positions, budget, recent, max_l
     a sequence over `budget` keeps its tokens of the last `recent` positions
     and of the others those of the largest weight, `budget` in all (keep
     recent <= budget: of more newest tokens than that, those in the lower slots
-    stay, not the latest); keys and values move in place.  weights float32 and positions int32 [batch, heads,
-    slots], seen int32 [batch] (see kv_append).  Returns, or writes to
-    ``out``, (weights, positions, lens) afterwards."""
+    stay, not the latest); keys and values move in place.  weights float32 and
+    positions int32 [batch, heads, slots], seen int32 [batch] (see kv_append).
+    Returns, or writes to ``out``, (weights, positions, lens) afterwards."""
     import torch
 
     here = _here()
