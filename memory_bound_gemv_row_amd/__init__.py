@@ -23,6 +23,8 @@ from .binding import (  # noqa: F401,E402  (no library load at import time)
     gemm_q8,
     PagedCache,
     paged_attention,
+    prompt_attention,
+    prefix_attention,
     kv_append,
     kv_evict,
 )

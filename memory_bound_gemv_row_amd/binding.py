@@ -1,6 +1,8 @@
 """ctypes binding over the C ABI in ``include/gemv.h``,
 ``include/gemv_quant.h``, ``include/gemv_softmax.h``,
-``include/gemv_tokens.h`` and ``include/gemv_attention.h``.
+``include/gemv_tokens.h``, ``include/gemv_attention.h``,
+``include/gemv_prompt.h``, ``include/gemv_rotate.h`` and
+``include/gemv_pages.h``.
 
 Argument marshalling only: every step of the product runs in the HIP
 library.  PyTorch supplies device memory and the current stream; no torch
@@ -110,6 +112,15 @@ def load():
         lib.gemv_kv_evict_workspace.restype = z
         lib.gemv_kv_evict.argtypes = [cache, batch, p, p, p, i64, i, i, p, p, p, p, z, p]
         lib.gemv_kv_evict.restype = i
+        f32 = ctypes.c_float
+        lib.gemv_prompt_attention_workspace.argtypes = [cache, batch, i, i, i, i, i]
+        lib.gemv_prompt_attention_workspace.restype = z
+        lib.gemv_prompt_attention.argtypes = [cache, batch, p, i, i, p, i64, i, f32, i, i, p, p, z, p]
+        lib.gemv_prompt_attention.restype = i
+        lib.gemv_prefix_attention_workspace.argtypes = [cache, batch, batch, i]
+        lib.gemv_prefix_attention_workspace.restype = z
+        lib.gemv_prefix_attention.argtypes = [cache, batch, p, batch, p, i64, i, f32, p, p, z, p]
+        lib.gemv_prefix_attention.restype = i
         _lib = lib
         return lib
 
@@ -615,7 +626,42 @@ def _tracked(t, name, dtype, batch, heads, room, here):
     return _ptr(t, name, dtype, (batch, heads, t.shape[2]), here)
 
 
-def paged_attention(cache, table, lens, q, scale=None, max_len=None, weights=None, out=None, stream=None):
+def _window(window, sinks):
+    """(window, sinks) as the C ABI takes them: window 0 is none."""
+    if window is None:
+        window = 0
+    elif window < 1:
+        raise ValueError(f"window {window} is below 1")
+    _dims(window, sinks)
+    return window, sinks
+
+
+def _attend(cache, batch, room, starts, rows, max_new, q, scale, window, sinks, out, stream, here):
+    """gemv_prompt_attention: `starts` is an address, or None for a row per sequence."""
+    import torch
+
+    heads, dim = q.shape[1], cache.head_dim
+    if q.shape[2] != dim or heads < 1 or heads % cache.heads:
+        raise ValueError(f"q: shape {tuple(q.shape)} does not fit {cache.heads} heads of {dim}")
+    qp, q_stride = _rows(q, "q", cache.dtype, (rows, heads, dim), here, heads * dim)
+    handle, empty = _work_stream(stream, here)
+    if out is None:
+        out = empty((rows, heads, dim), dtype=cache.dtype, device=cache.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", cache.dtype, (rows, heads, dim), here)
+    scale = dim ** -0.5 if scale is None else scale
+    lib, c, s = load(), cache._by_ref, ctypes.byref(batch)
+    need = cache._need(("rows", batch.batch, rows, max_new, heads, room, window, sinks),
+                       lambda: lib.gemv_prompt_attention_workspace(c, s, rows, max_new, heads, window, sinks))
+    work = empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    _check(lib.gemv_prompt_attention(c, s, starts, rows, max_new, qp, q_stride, heads, scale, window, sinks, op,
+                                     work.data_ptr() if need else None, need, handle), "gemv_prompt_attention")
+    return out
+
+
+def paged_attention(cache, table, lens, q, scale=None, max_len=None, weights=None, out=None, stream=None, window=None,
+                    sinks=0):
     """Attention of one new token per sequence over a paged cache: q
     [batch, q_heads, head_dim] of the cache's type (sequences may lie apart)
     -> [batch, q_heads, head_dim].  table int32 [batch, pages per sequence],
@@ -623,11 +669,19 @@ def paged_attention(cache, table, lens, q, scale=None, max_len=None, weights=Non
     longest length, where the host knows one below the table's room.
     weights float32 [batch, heads, slots]: each token's attention weights,
     summed over the query heads of its head, are added to it.  out may be a
-    dense q itself."""
+    dense q itself.  With a window, a sequence's newest `window` tokens are seen,
+    and its first `sinks`; weights are not kept then."""
     import torch
 
     here = _here()
     batch, room = cache._batch(table, lens, max_len, here)
+    if window is not None:
+        if weights is not None:
+            raise ValueError("weights are not kept where a window is seen")
+        if q.dim() != 3 or q.shape[0] != batch.batch:
+            raise ValueError(f"q: shape {tuple(q.shape)} does not fit {batch.batch} sequences")
+        window, sinks = _window(window, sinks)
+        return _attend(cache, batch, room, None, batch.batch, 1, q, scale, window, sinks, out, stream, here)
     B, heads, dim = q.shape
     if B != batch.batch or dim != cache.head_dim or heads < 1 or heads % cache.heads:
         raise ValueError(f"q: shape {tuple(q.shape)} does not fit {batch.batch} sequences, {cache.heads} heads of "
@@ -648,6 +702,67 @@ def paged_attention(cache, table, lens, q, scale=None, max_len=None, weights=Non
     work = empty(need, dtype=torch.uint8, device=cache.device) if need else None
     _check(lib.gemv_attention(c, s, qp, q_stride, heads, scale, op, wp, slots, work.data_ptr() if need else None, need,
                               handle), "gemv_attention")
+    return out
+
+
+def prompt_attention(cache, table, lens, starts, q, scale=None, max_len=None, max_new=None, window=None, sinks=0, out=None,
+                     stream=None):
+    """Causal attention of the newest tokens of each sequence, which the cache
+    holds already: rows starts[b] .. starts[b+1] - 1 of q [rows, q_heads,
+    head_dim] of the cache's type (rows may lie apart) are the last tokens of
+    sequence b -> [rows, q_heads, head_dim].  table int32 [batch, pages per
+    sequence], lens and starts int32 [batch] and [batch + 1]; max_new and
+    max_len the most new tokens and the longest length, where the host knows
+    ones below the rows and the table's room.  With a window, a token sees the
+    `window` tokens up to itself, and the sequence's first `sinks`.  Rows of no
+    sequence stay as they are in `out`, which may be a dense q itself."""
+    import torch
+
+    here = _here()
+    batch, room = cache._batch(table, lens, max_len, here)
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, head_dim]")
+    rows = q.shape[0]
+    max_new = rows if max_new is None else max_new
+    _dims(rows, max_new)
+    sp = _ptr(starts, "starts", torch.int32, (batch.batch + 1,), here)
+    window, sinks = _window(window, sinks)
+    return _attend(cache, batch, room, sp, rows, max_new, q, scale, window, sinks, out, stream, here)
+
+
+def prefix_attention(cache, prefix_table, prefix_lens, starts, table, lens, q, scale=None, max_prefix=None, max_len=None,
+                     out=None, stream=None):
+    """Attention of one new token per sequence, where groups of sequences share
+    a prefix: sequences starts[g] .. starts[g+1] - 1 see the prefix_lens[g]
+    tokens in the pages of prefix_table[g], and then their own lens[b] in those
+    of table[b].  q [batch, q_heads, head_dim] of the cache's type -> the same
+    shape; tables and counts int32 (prefix_table [groups, pages], starts
+    [groups + 1]); max_prefix and max_len the longest prefix and length, where
+    the host knows ones below the tables' room.  out may be a dense q itself."""
+    import torch
+
+    here = _here()
+    batch, room = cache._batch(table, lens, max_len, here)
+    prefixes, far = cache._batch(prefix_table, prefix_lens, max_prefix, here)
+    B, heads, dim = q.shape
+    if B != batch.batch or dim != cache.head_dim or heads < 1 or heads % cache.heads:
+        raise ValueError(f"q: shape {tuple(q.shape)} does not fit {batch.batch} sequences, {cache.heads} heads of "
+                         f"{cache.head_dim}")
+    sp = _ptr(starts, "starts", torch.int32, (prefixes.batch + 1,), here)
+    qp, q_stride = _rows(q, "q", cache.dtype, (B, heads, dim), here, heads * dim)
+    handle, empty = _work_stream(stream, here)
+    if out is None:
+        out = empty((B, heads, dim), dtype=cache.dtype, device=cache.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", cache.dtype, (B, heads, dim), here)
+    scale = dim ** -0.5 if scale is None else scale
+    lib, c, f, s = load(), cache._by_ref, ctypes.byref(prefixes), ctypes.byref(batch)
+    need = cache._need(("prefix", prefixes.batch, far, B, heads, room),
+                       lambda: lib.gemv_prefix_attention_workspace(c, f, s, heads))
+    work = empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    _check(lib.gemv_prefix_attention(c, f, sp, s, qp, q_stride, heads, scale, op, work.data_ptr() if need else None, need,
+                                     handle), "gemv_prefix_attention")
     return out
 
 

@@ -4,8 +4,9 @@
 ``csrc/gemv_api.hip`` (GEMV, which includes its kernels),
 ``csrc/quant_api.hip`` (the weight quantiser), ``csrc/softmax_api.hip``
 (the row softmax), ``csrc/tokens_api.hip`` (the INT8 product of several
-tokens) and ``csrc/attention_api.hip`` (attention over a paged key-value
-cache and the cache's upkeep) into one library,
+tokens), ``csrc/attention_api.hip`` (attention over a paged key-value cache
+and the cache's upkeep) and ``csrc/prompt_api.hip`` (attention of several
+tokens, through a window and behind shared prefixes) into one library,
 ``memory_bound_gemv_row_amd/libgemv_amd.so``.
 """
 from __future__ import annotations
@@ -20,11 +21,13 @@ SRC_DIR = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemv_amd.so")
 SOURCES = [os.path.join(SRC_DIR, f) for f in ("gemv_api.hip", "quant_api.hip", "softmax_api.hip", "tokens_api.hip",
-                                                 "attention_api.hip")]
+                                                 "attention_api.hip", "prompt_api.hip")]
 DEPENDS = SOURCES + [os.path.join(SRC_DIR, f) for f in ("gemv_kernels.hpp", "quant_kernels.hpp", "softmax_kernels.hpp",
-                                                    "tokens_kernels.hpp", "attention_kernels.hpp", "device_info.hpp")] \
+                                                    "tokens_kernels.hpp", "paged.hpp", "attention_kernels.hpp",
+                                                    "cache_kernels.hpp", "prompt_kernels.hpp", "attention_host.hpp",
+                                                    "device_info.hpp")] \
     + [os.path.join(INCLUDE, f) for f in ("gemv.h", "gemv_quant.h", "gemv_softmax.h", "gemv_types.h", "gemv_tokens.h",
-                                             "gemv_attention.h")]
+                                             "gemv_attention.h", "gemv_prompt.h")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -36,6 +39,7 @@ HIPCC_FLAGS = [
     "-Wall",
     "-Wextra",
     "-Werror",          # host and device warnings fail the build
+    "-parallel-jobs=8",
     # no packed FP32 instructions in device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]

@@ -1,0 +1,435 @@
+// prompt_api.hip -- C ABI of attention with several new tokens per sequence, with
+// a window, and behind shared prefixes (declared in include/gemv_prompt.h):
+// validation, workspaces, geometry and launch.
+#include "gemv_prompt.h"
+
+#include "attention_host.hpp"
+#include "prompt_kernels.hpp"
+
+#include <float.h>
+#include <math.h>
+
+namespace gattn {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// How query rows and keys are split: places for row tiles of a key-value head,
+// parts of the keys and tiles of keys in each.
+struct Tiling {
+    int64_t tiles;
+    int parts, chunk;
+    size_t ms_at, out_at, bytes;
+};
+
+// The least estimate, in tiles of keys, of what the busiest CU does: rounds of
+// two workgroups per CU (one for heads over 128), with `kStart` for a
+// workgroup's start and end and `kJoin` for a join.
+Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int limit, int window, int sinks, int cus)
+{
+    constexpr int kStart = 3, kJoin = 4;
+    Tiling t{};
+    t.tiles = rows * group / kTileRows + batch;
+    int64_t keys = ((int64_t)limit + kTileKeys - 1) / kTileKeys;
+    if (window > 0) {
+        const int64_t near = ((int64_t)window + kTileRows / group + kTileKeys) / kTileKeys + 1;
+        const int64_t seen = ((int64_t)sinks + kTileKeys - 1) / kTileKeys + near;
+        keys = seen < keys ? seen : keys;
+    }
+    keys = keys > 0 ? keys : 1;
+    const int64_t each = (rows + batch - 1) / (batch > 0 ? batch : 1);   // new tokens of a sequence, about
+    const int64_t items = (int64_t)c->heads * batch * ((each * group + kTileRows - 1) / kTileRows);
+    const int64_t slots = (int64_t)cus * (c->head_dim > 128 ? 1 : 2);
+    int64_t least = INT64_MAX;
+    for (int64_t parts = 1; parts <= keys && parts <= 256; ++parts) {
+        const int64_t chunk = (keys + parts - 1) / parts;
+        if ((keys + chunk - 1) / chunk != parts)
+            continue;
+        const int64_t cost = (items * parts + slots - 1) / slots * (chunk + kStart) + (parts > 1 ? kJoin + parts / 16 : 0);
+        if (cost < least) {
+            least = cost;
+            t.parts = (int)parts;
+            t.chunk = (int)chunk;
+        }
+    }
+    return t;
+}
+
+void place_parts(Tiling* t, size_t at, int64_t heads, int dim, bool kept)
+{
+    t->ms_at = at;
+    t->out_at = t->bytes = at;
+    if (!kept)
+        return;
+    t->out_at = at + round16((size_t)heads * t->parts * 2 * sizeof(float));
+    t->bytes = t->out_at + round16((size_t)heads * t->parts * dim * sizeof(float));
+}
+
+// The slots that a single new token sees, in whole tiles of decode attention.
+int seen_slots(int limit, int window, int sinks16)
+{
+    const int64_t seen = (int64_t)sinks16 + window + 15;
+    return window > 0 && seen < limit ? (int)seen : limit;
+}
+
+// A window that no sequence is longer than hides nothing.
+int narrow_window(int window, int limit) { return window < limit ? window : 0; }
+
+int whole_sinks(int sinks, int tile, int limit)
+{
+    const int64_t n = ((int64_t)sinks + tile - 1) / tile * tile;
+    const int64_t most = ((int64_t)limit + tile - 1) / tile * tile;
+    return (int)(n < most ? n : most);
+}
+
+template <int DT, bool WHOLE, int WAVES>
+const void* view_sized(int dim)
+{
+    if constexpr (WHOLE) {
+        if (dim == 64)
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 64, true, true, WAVES, true>);
+        if (dim == 128)
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 128, true, true, WAVES, true>);
+        if (dim == 256)
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 256, true, true, WAVES, true>);
+    }
+    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64, WHOLE, false, WAVES, true>)
+           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128, WHOLE, false, WAVES, true>)
+                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256, WHOLE, false, WAVES, true>);
+}
+
+template <int DT>
+const void* view_for(const gemv_kv_cache* c, bool lone)
+{
+    return lone             ? view_sized<DT, true, kLoneWaves>(c->head_dim)
+           : whole_tiles(c) ? view_sized<DT, true, kWaves>(c->head_dim)
+                            : view_sized<DT, false, kWaves>(c->head_dim);
+}
+
+template <int DT, bool WHOLE>
+const void* prompt_sized(int dim)
+{
+    if constexpr (WHOLE) {
+        if (dim == 64)
+            return reinterpret_cast<const void*>(&prompt_kernel<DT, 64, true, true>);
+        if (dim == 96)
+            return reinterpret_cast<const void*>(&prompt_kernel<DT, 96, true, true>);
+        if (dim == 128)
+            return reinterpret_cast<const void*>(&prompt_kernel<DT, 128, true, true>);
+        if (dim == 256)
+            return reinterpret_cast<const void*>(&prompt_kernel<DT, 256, true, true>);
+    }
+    return dim <= 64    ? reinterpret_cast<const void*>(&prompt_kernel<DT, 64, WHOLE, false>)
+           : dim <= 96  ? reinterpret_cast<const void*>(&prompt_kernel<DT, 96, WHOLE, false>)
+           : dim <= 128 ? reinterpret_cast<const void*>(&prompt_kernel<DT, 128, WHOLE, false>)
+                        : reinterpret_cast<const void*>(&prompt_kernel<DT, 256, WHOLE, false>);
+}
+
+const void* prompt_for(const gemv_kv_cache* c)
+{
+    if (c->dtype == GEMV_F16)
+        return whole_tiles(c) ? prompt_sized<kF16, true>(c->head_dim) : prompt_sized<kF16, false>(c->head_dim);
+    return whole_tiles(c) ? prompt_sized<kBF16, true>(c->head_dim) : prompt_sized<kBF16, false>(c->head_dim);
+}
+
+int join_parts(const Join& j, int dtype, hipStream_t stream)
+{
+    void* args[] = {(void*)&j};
+    const int64_t grid = ((int64_t)j.rows * j.q_heads + 3) / 4;
+    return launch(dtype == GEMV_F16 ? reinterpret_cast<const void*>(&join_parts_kernel<kF16>)
+                                    : reinterpret_cast<const void*>(&join_parts_kernel<kBF16>), grid, 256, args, stream);
+}
+
+bool joins_fit(int64_t rows, int q_heads) { return fits((rows * q_heads + 3) / 4, 256); }
+
+// Single new tokens, by the kernel of decode attention.  `at.limit` and
+// `split` are for the slots seen.
+Attention newest(const gemv_kv_cache* c, const Pages& at, int batch, const Split& split, const void* q, int64_t q_stride,
+                 int q_heads, float scale, char* ws, size_t ms_at, size_t out_at, bool kept)
+{
+    Attention a{};
+    a.at = at;
+    a.k = static_cast<const uint16_t*>(c->k);
+    a.v = static_cast<const uint16_t*>(c->v);
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_stride = q_stride;
+    a.batch = batch;
+    a.q_heads = q_heads;
+    a.heads = c->heads;
+    a.dim = c->head_dim;
+    a.group = q_heads / c->heads;
+    a.tiles = split.tiles;
+    a.parts = split.parts;
+    a.chunk = split.chunk;
+    a.scale = scale * kLog2e;
+    a.part_ms = kept ? reinterpret_cast<float*>(ws + ms_at) : nullptr;
+    a.part_out = kept ? reinterpret_cast<float*>(ws + out_at) : nullptr;
+    a.partial = kept;
+    return a;
+}
+
+int64_t newest_grid(const gemv_kv_cache* c, int batch, const Split& p)
+{
+    const int64_t ranges = (int64_t)batch * p.parts;
+    return c->heads * (p.tiles > 1 ? (ranges + 7) / 8 * 8 * p.tiles : ranges);
+}
+
+// Rows of several tokens per sequence, or of a group.
+Prompt tiled(const gemv_kv_cache* c, const Pages& at, int batch, const int32_t* starts, int rows, const Tiling& t,
+             const void* q, int64_t q_stride, int q_heads, float scale, char* ws, bool kept)
+{
+    Prompt a{};
+    a.at = at;
+    a.k = static_cast<const uint16_t*>(c->k);
+    a.v = static_cast<const uint16_t*>(c->v);
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_stride = q_stride;
+    a.starts = starts;
+    a.batch = batch;
+    a.rows = rows;
+    a.max_new = rows;
+    a.q_heads = q_heads;
+    a.heads = c->heads;
+    a.dim = c->head_dim;
+    a.group = q_heads / c->heads;
+    a.group_of = divider(a.group);
+    a.tiles = (int)t.tiles;
+    a.parts = t.parts;
+    a.chunk = t.chunk;
+    const float size = fabsf(scale) * kLog2e;
+    a.scale = size == 0.0f ? 1.0f : size;
+    a.keep = size == 0.0f ? 0u : ~0u;
+    a.flip = scale < 0 ? 0x80008000u : 0u;
+    a.slack = kSlack / a.scale < FLT_MAX ? kSlack / a.scale : FLT_MAX;
+    a.part_ms = kept ? reinterpret_cast<float*>(ws + t.ms_at) : nullptr;
+    a.part_out = kept ? reinterpret_cast<float*>(ws + t.out_at) : nullptr;
+    return a;
+}
+
+struct Plan {
+    bool single;        // one new token: the kernel of decode attention
+    bool joined;
+    int window, sinks;
+    Split split;        // single
+    Tiling tiling;      // otherwise
+    size_t ms_at, out_at, bytes;
+};
+
+Plan plan_prompt(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int rows, int max_new, int q_heads, int window,
+                 int sinks, int cus)
+{
+    Plan p{};
+    p.window = narrow_window(window, limit);
+    p.sinks = p.window > 0 ? sinks : 0;
+    p.single = max_new == 1;
+    const int64_t heads = (int64_t)rows * q_heads;
+    if (p.single) {
+        p.split = split_for(c, s, seen_slots(limit, p.window, whole_sinks(p.sinks, 16, limit)), q_heads, false, cus);
+        p.joined = p.split.parts > 1;
+        p.ms_at = 0;
+        p.out_at = p.joined ? round16((size_t)heads * p.split.parts * 2 * sizeof(float)) : 0;
+        p.bytes = p.joined ? p.out_at + (size_t)heads * p.split.parts * c->head_dim * sizeof(float) : 0;
+        return p;
+    }
+    p.tiling = tile_rows(c, rows, s->batch, q_heads / c->heads, limit, p.window, p.sinks, cus);
+    p.joined = p.tiling.parts > 1;
+    place_parts(&p.tiling, 0, heads, c->head_dim, p.joined);
+    p.bytes = p.tiling.bytes;
+    return p;
+}
+
+struct PrefixPlan {
+    Tiling shared;
+    Split own;
+    size_t own_ms_at, own_out_at, bytes;
+};
+
+PrefixPlan plan_prefix(const gemv_kv_cache* c, const gemv_kv_batch* prefixes, const gemv_kv_batch* s, int far_limit,
+                       int limit, int q_heads, int cus)
+{
+    PrefixPlan p{};
+    const int64_t heads = (int64_t)s->batch * q_heads;
+    p.shared = tile_rows(c, s->batch, prefixes->batch, q_heads / c->heads, far_limit, 0, 0, cus);
+    if (prefixes->batch == 0 || far_limit == 0)
+        p.shared.parts = 0;
+    place_parts(&p.shared, 0, heads, c->head_dim, true);
+    p.own = split_for(c, s, limit, q_heads, false, cus);
+    if (limit == 0)
+        p.own.parts = 0;
+    p.own_ms_at = p.shared.bytes;
+    p.own_out_at = p.own_ms_at + round16((size_t)heads * p.own.parts * 2 * sizeof(float));
+    p.bytes = p.own_out_at + (size_t)heads * p.own.parts * c->head_dim * sizeof(float);
+    return p;
+}
+
+int check_query(const gemv_kv_cache* c, const void* q, int64_t q_stride, const void* out)
+{
+    if (q == nullptr || out == nullptr)
+        return GEMV_E_INVAL;
+    (void)c;
+    return q_stride % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) ? GEMV_E_UNSUPPORTED : GEMV_OK;
+}
+
+bool holds(const void* workspace, size_t bytes, size_t need)
+{
+    return need == 0 || (workspace != nullptr && bytes >= need && aligned(workspace, 16));
+}
+
+}  // namespace
+}  // namespace gattn
+
+extern "C" {
+
+size_t gemv_prompt_attention_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* batch, int rows, int max_new,
+                                       int q_heads, int window, int sinks)
+{
+    using namespace gattn;
+    Pages at{};
+    if (check(cache, batch, &at) != GEMV_OK || q_heads < 1 || q_heads % cache->heads != 0 || rows < 1 || max_new < 1 ||
+        window < 0 || sinks < 0 || batch->batch == 0)
+        return 0;
+    gemv_device::Device dev{};
+    if (gemv_device::current(&dev) != GEMV_OK)
+        return 0;
+    return plan_prompt(cache, batch, at.limit, rows, max_new, q_heads, window, sinks, dev.cus).bytes;
+}
+
+int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch, const int32_t* starts, int rows,
+                          int max_new, const void* q, int64_t q_stride, int q_heads, float scale, int window, int sinks,
+                          void* out, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    using namespace gattn;
+    Pages at{};
+    if (int rc = check(cache, batch, &at); rc != GEMV_OK)
+        return rc;
+    if (rows < 0 || max_new < 0 || window < 0 || sinks < 0 || q_heads < 1 || q_heads % cache->heads != 0 ||
+        q_stride < (int64_t)q_heads * cache->head_dim)
+        return GEMV_E_INVAL;
+    if (starts == nullptr && batch->batch > 0 && (max_new != 1 || rows < batch->batch))
+        return GEMV_E_INVAL;
+    if (batch->batch == 0 || rows == 0 || max_new == 0)
+        return GEMV_OK;
+    if (int rc = check_query(cache, q, q_stride, out); rc != GEMV_OK)
+        return rc;
+    gemv_device::Device dev{};
+    if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
+        return rc;
+    const Plan p = plan_prompt(cache, batch, at.limit, rows, max_new, q_heads, window, sinks, dev.cus);
+    if (!holds(workspace, workspace_bytes, p.bytes))
+        return GEMV_E_INVAL;
+    char* ws = static_cast<char*>(workspace);
+    Join j{};
+    j.rows = starts != nullptr ? rows : batch->batch;
+    j.q_heads = q_heads;
+    j.dim = cache->head_dim;
+    j.starts = starts;
+    j.batch = batch->batch;
+    j.max_new = max_new;
+    j.out = out;
+    if (p.joined && !joins_fit(rows, q_heads))
+        return GEMV_E_UNSUPPORTED;
+    if (p.single) {
+        Attention a = newest(cache, at, batch->batch, p.split, q, q_stride, q_heads, scale, ws, p.ms_at, p.out_at, p.joined);
+        a.out = out;
+        a.starts = starts;
+        a.rows = rows;
+        a.window = p.window;
+        a.sinks = p.sinks;
+        a.sinks16 = whole_sinks(p.sinks, 16, at.limit);
+        const int64_t grid = newest_grid(cache, batch->batch, p.split);
+        const int block = (p.split.lone ? kLoneWaves : kWaves) * 64;
+        if (!fits(grid, block))
+            return GEMV_E_UNSUPPORTED;
+        void* args[] = {(void*)&a};
+        const void* fn = cache->dtype == GEMV_F16 ? view_for<kF16>(cache, p.split.lone) : view_for<kBF16>(cache, p.split.lone);
+        if (int rc = launch(fn, grid, block, args, stream); rc != GEMV_OK || !p.joined)
+            return rc;
+        j.from[0] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
+        return join_parts(j, cache->dtype, stream);
+    }
+    const int64_t grid = p.tiling.tiles * cache->heads * p.tiling.parts;
+    if (!fits(grid, 256))
+        return GEMV_E_UNSUPPORTED;
+    Prompt a = tiled(cache, at, batch->batch, starts, rows, p.tiling, q, q_stride, q_heads, scale, ws, p.joined);
+    a.causal = true;
+    a.max_new = max_new < rows ? max_new : rows;
+    a.window = p.window;
+    a.sinks = p.sinks;
+    a.sink_tiles = whole_sinks(p.sinks, kTileKeys, at.limit) / kTileKeys;
+    a.out = out;
+    void* args[] = {(void*)&a};
+    if (int rc = launch(prompt_for(cache), grid, 256, args, stream); rc != GEMV_OK || !p.joined)
+        return rc;
+    j.from[0] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
+    return join_parts(j, cache->dtype, stream);
+}
+
+size_t gemv_prefix_attention_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* prefixes,
+                                       const gemv_kv_batch* batch, int q_heads)
+{
+    using namespace gattn;
+    Pages at{}, far{};
+    if (check(cache, batch, &at) != GEMV_OK || check(cache, prefixes, &far) != GEMV_OK || q_heads < 1 ||
+        q_heads % cache->heads != 0 || batch->batch == 0)
+        return 0;
+    gemv_device::Device dev{};
+    if (gemv_device::current(&dev) != GEMV_OK)
+        return 0;
+    return plan_prefix(cache, prefixes, batch, far.limit, at.limit, q_heads, dev.cus).bytes;
+}
+
+int gemv_prefix_attention(const gemv_kv_cache* cache, const gemv_kv_batch* prefixes, const int32_t* starts,
+                          const gemv_kv_batch* batch, const void* q, int64_t q_stride, int q_heads, float scale, void* out,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    using namespace gattn;
+    Pages at{}, far{};
+    if (int rc = check(cache, batch, &at); rc != GEMV_OK)
+        return rc;
+    if (int rc = check(cache, prefixes, &far); rc != GEMV_OK)
+        return rc;
+    if (q_heads < 1 || q_heads % cache->heads != 0 || q_stride < (int64_t)q_heads * cache->head_dim)
+        return GEMV_E_INVAL;
+    if (prefixes->batch > 0 && starts == nullptr)
+        return GEMV_E_INVAL;
+    if (batch->batch == 0)
+        return GEMV_OK;
+    if (int rc = check_query(cache, q, q_stride, out); rc != GEMV_OK)
+        return rc;
+    gemv_device::Device dev{};
+    if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
+        return rc;
+    const PrefixPlan p = plan_prefix(cache, prefixes, batch, far.limit, at.limit, q_heads, dev.cus);
+    if (!holds(workspace, workspace_bytes, p.bytes))
+        return GEMV_E_INVAL;
+    const int64_t far_grid = p.shared.tiles * cache->heads * p.shared.parts;
+    const int64_t grid = p.own.parts > 0 ? newest_grid(cache, batch->batch, p.own) : 0;
+    const int block = (p.own.lone ? kLoneWaves : kWaves) * 64;
+    if (!fits(far_grid, 256) || !fits(grid, block) || !joins_fit(batch->batch, q_heads))
+        return GEMV_E_UNSUPPORTED;
+    char* ws = static_cast<char*>(workspace);
+    Join j{};
+    j.rows = batch->batch;
+    j.q_heads = q_heads;
+    j.dim = cache->head_dim;
+    j.out = out;
+    if (far_grid > 0) {
+        Prompt a = tiled(cache, far, prefixes->batch, starts, batch->batch, p.shared, q, q_stride, q_heads, scale, ws, true);
+        void* args[] = {(void*)&a};
+        if (int rc = launch(prompt_for(cache), far_grid, 256, args, stream); rc != GEMV_OK)
+            return rc;
+        j.from[0] = Source{a.part_ms, a.part_out, a.parts, starts, prefixes->batch};
+    }
+    if (grid > 0) {
+        Attention a = newest(cache, at, batch->batch, p.own, q, q_stride, q_heads, scale, ws, p.own_ms_at, p.own_out_at, true);
+        a.rows = batch->batch;
+        void* args[] = {(void*)&a};
+        const void* fn = cache->dtype == GEMV_F16 ? view_for<kF16>(cache, p.own.lone) : view_for<kBF16>(cache, p.own.lone);
+        if (int rc = launch(fn, grid, block, args, stream); rc != GEMV_OK)
+            return rc;
+        j.from[1] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
+    }
+    return join_parts(j, cache->dtype, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,690 @@
+// prompt_kernels.hpp -- gfx950 (CDNA4) device code for attention of many query
+// rows over a paged key-value cache: several new tokens per sequence, and the
+// shared prefix of a group of sequences.
+//
+//   o_r = sum_j p_rj v_j,  p_r = softmax_j(scale * q_r . k_j),  j visible to r
+//
+// Both products are matrix products with the keys read once for 128 rows, so
+// long prompts are bound by the matrix units and the exponentials between the
+// two products, few rows by memory.
+#pragma once
+
+#include "paged.hpp"
+
+namespace gattn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTileRows = 128;   // query rows of a workgroup, 32 a wave
+constexpr int kTileKeys = 64;    // keys of a step, 16 loaded by each wave
+constexpr int kEverySlot = 0x7FFFFFFE;
+
+struct Prompt {
+    Pages at;
+    const uint16_t* k;
+    const uint16_t* v;
+    const uint16_t* q;
+    int64_t q_stride;
+    const int32_t* starts;   // [batch + 1]: rows of q of each sequence
+    int batch, rows, max_new;
+    int q_heads, heads, dim;
+    int group;               // query heads per key-value head
+    Divider group_of;
+    bool causal;
+    int window;              // tokens seen, the row's own included; 0: all
+    int sinks, sink_tiles;   // first tokens seen all the same, and the tiles that hold them
+    int tiles;               // places for row tiles per key-value head: rows * group / 128 + batch
+    int parts, chunk;        // workgroups over the keys, and tiles of keys of each
+    float scale;             // of the logits, above zero, log2(e) included
+    float slack;             // kSlack / scale
+    unsigned keep, flip;     // bits of q: none where the scale is zero; the signs flipped where it is negative
+    void* out;
+    float* part_out;         // [rows][q_heads][parts][dim], not divided by the sums, or null
+    float* part_ms;          // [rows][q_heads][parts][2]: maximum and sum of powers
+};
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma_wide(u32x4 a, u32x4 b, f32x16 c)
+{
+    if constexpr (DT == kF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <int DT>
+__device__ __forceinline__ unsigned narrow_pair(float x, float y)
+{
+    const f32x2 v = {x, y};
+    if constexpr (DT == kF16)
+        return __builtin_bit_cast(unsigned, __builtin_convertvector(v, f16x2));
+    else
+        return __builtin_bit_cast(unsigned, __builtin_convertvector(v, bf16x2));
+}
+
+// sum + both elements of a pair
+template <int DT>
+__device__ __forceinline__ float add_pair([[maybe_unused]] unsigned pair, float sum)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    if constexpr (DT == kF16)
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), f16x2{(_Float16)1.0f, (_Float16)1.0f}, sum, false);
+    else
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), bf16x2{(__bf16)1.0f, (__bf16)1.0f}, sum, false);
+#else
+    return sum;
+#endif
+}
+
+// Sixteen bytes of each lane straight to LDS, to its place behind byte `to` (the
+// same for all lanes).  Written out, for the compiler would make every read of
+// LDS wait for such loads, those into the other buffer too; the kernel waits for
+// them itself, before the barrier that hands a buffer over.  s_nop: five steps
+// between a vector instruction that writes a scalar register and its use as a
+// descriptor, and one after m0 is set.
+__device__ __forceinline__ void piece_to_lds([[maybe_unused]] u32x4 from, [[maybe_unused]] unsigned offset,
+                                             [[maybe_unused]] unsigned to)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :: "s"(to), "v"(offset), "s"(from) : "memory");
+#endif
+}
+
+__device__ __forceinline__ void piece_to_lds([[maybe_unused]] const void* from, [[maybe_unused]] unsigned to)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(to), "v"(from) : "memory");
+#endif
+}
+
+// Byte address of LDS memory.
+__device__ __forceinline__ unsigned lds_byte([[maybe_unused]] const void* p)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+#else
+    return 0;
+#endif
+}
+
+// A buffer descriptor as four words, the same for all lanes.
+__device__ __forceinline__ u32x4 descriptor(const uint16_t* p, unsigned bytes)
+{
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    return u32x4{(unsigned)at, (unsigned)(at >> 32) & 0xFFFFu, bytes, 0x00027000u};
+}
+
+// A word that no kernel running at the same time writes, at an address that
+// all lanes share.
+__device__ __forceinline__ int shared_word(const int32_t* p)
+{
+    return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
+}
+
+// Four keys of one column: within 16 lanes, lane i points at four elements of
+// row i / 4, columns 4 (i % 4) on, and gets column i of the four rows.
+__device__ __forceinline__ u32x2 column_of_four([[maybe_unused]] const u32x4* base, [[maybe_unused]] unsigned byte)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    auto p = (__attribute__((address_space(3))) const char*)base + byte;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+#else
+    return u32x2{0, 0};
+#endif
+}
+
+__device__ __forceinline__ unsigned bits_below(int64_t n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// The sequence whose row tiles hold place `u`, of places that a sequence b has
+// from floor(starts[b] * group / 128) + b on: as many as it can need, none
+// twice.  A wave looks at 64 sequences at a time.
+__device__ __forceinline__ int sequence_at(const int32_t* starts, int batch, int rows, int group, int64_t u)
+{
+    const int lane = threadIdx.x & 63;
+    int low = 0, count = batch;   // the answer is in [low, low + count)
+    while (count > 1) {
+        const int step = (count + 63) / 64;
+        const int at = lane * step;
+        const bool below = at < count && row_start(starts, low + at, rows) * group / kTileRows + low + at <= u;
+        const int n = __popcll(__ballot(below));   // the places rise with the sequence
+        const int first = n > 0 ? (n - 1) * step : 0;
+        low += first;
+        count = count - first < step ? count - first : step;
+    }
+    return low;
+}
+
+// 16 zeros that slots without a page are read from
+__device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
+
+// One workgroup: 128 query rows (tokens times the query heads of one key-value
+// head, a token's heads together) of one sequence, over one part of the keys
+// that any of them sees.  Each wave has 32 rows; the four load 64 keys and
+// values at a time straight to LDS, into one of two buffers while the other is
+// multiplied.
+//
+// Logits: v_mfma_f32_32x32x16 with keys as rows and queries, which stay in
+// registers, as columns: lane l gets, for query row l % 32, the logits of keys
+// 8 (i / 4) + 4 (l / 32) + i % 4, i = 0..15.  A lane so has one query row: its
+// maximum and sum need no other lane but l ^ 32's, and that only when the
+// maximum moves (past it by kSlack, as in decode attention) and at the end.
+// The powers, in pairs rounded to 16 bits, are in place as the right operand of
+// the product with the values, if that takes its summed index in the same
+// order of keys; the left operand, columns of four values, comes out of LDS
+// turned by ds_read_b64_tr_b16.  The powers' rounding, half a step of 2^-11 or
+// 2^-8 relative each, is below that of the output, which averages over them;
+// the sum is taken over the rounded powers, so the weights still add up to one.
+//
+// Places in LDS: piece c (16 bytes) of key row r lies at c ^ swizzle(r), such
+// that the 16 rows that a read of keys takes at a time, and the four rows of
+// 64 bytes that a read of values does, are in different banks.
+//
+// Masks are looked at in tiles that some row of the workgroup does not see whole.
+// There the values may hold NaN or infinities in slots that only some rows
+// see; 0 * NaN would bring them to the others, so where there are any such a tile
+// is multiplied key by key, and rows that do not see the key keep their sums.
+template <int DT, int DP, bool WHOLE, bool EXACT>
+__global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
+prompt_kernel(Prompt a)
+{
+    constexpr int CH = DP / 8;        // pieces of a row
+    constexpr int kLoads = CH / 4;    // 64 pieces each of the 16 rows that a wave loads
+    constexpr int kSteps = DP / 16;   // of 16 elements of the dot products
+    constexpr int kBlocks = DP / 32;  // of 32 elements of the output
+    __shared__ u32x4 buffers[2][2][kTileKeys * CH];                    // keys and values of a step, and of the next
+    __shared__ __attribute__((aligned(8))) uint16_t held_bits[2][4];   // bit per key: its slot is there
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5;
+
+    // Workgroups go to the eight XCDs in turn.  Those that read the same keys
+    // (a head's, of a part) follow each other on one XCD where such sets are a
+    // multiple of eight; the last rows, which see most, come first.
+    const int sets = a.heads * a.parts;
+    int set, place;
+    if (sets % 8 == 0) {
+        const int j = (int)blockIdx.x >> 3, m = j / a.tiles;
+        set = m * 8 + ((int)blockIdx.x & 7);
+        place = j - m * a.tiles;
+    } else {
+        place = (int)blockIdx.x / sets;
+        set = (int)blockIdx.x - place * sets;
+    }
+    const int kv = set % a.heads, part = set / a.heads;
+    place = a.tiles - 1 - place;
+    const int b = __builtin_amdgcn_readfirstlane(sequence_at(a.starts, a.batch, a.rows, a.group, place));
+    const int64_t from = row_start(a.starts, b, a.rows), to = row_start(a.starts, b + 1, a.rows);
+    int64_t n64 = to - from;
+    n64 = n64 < a.max_new ? n64 : a.max_new;
+    const int n = __builtin_amdgcn_readfirstlane((int)n64);                     // new tokens
+    const int64_t row0 = to - n64;                                              // the first of them
+    const int64_t r0 = (place - from * a.group / kTileRows - b) * kTileRows;   // this tile's first row
+    if (n <= 0 || r0 < 0 || r0 >= (int64_t)n * a.group)
+        return;
+    const int len = __builtin_amdgcn_readfirstlane(a.at.length(b));
+    const int rows = (int)((int64_t)n * a.group - r0 < kTileRows ? (int64_t)n * a.group - r0 : kTileRows);
+
+    // tokens of the tile and of this wave, and the slots they see
+    const int64_t token0 = r0 / a.group;
+    const int head_shift = (int)(r0 - token0 * a.group);                        // r0 is head_shift rows past its token's first
+    auto token_of = [&](int r) { return (int)token0 + a.group_of.by(r + head_shift); };
+    // position of a row's token, the last slot that it sees; -1: none
+    auto position_of = [&](int r) {
+        const int p = len - n + token_of(r);
+        return !a.causal ? kEverySlot : p > -1 ? p : -1;
+    };
+    const int tile_min = position_of(0), tile_max = position_of(rows - 1);
+    const bool mine = 32 * wave < rows;
+    const int last = rows - 1 < 32 * wave + 31 ? rows - 1 : 32 * wave + 31;
+    const int wave_min = position_of(mine ? 32 * wave : 0), wave_max = position_of(last);
+    const int top_slot = tile_max + 1 < len ? tile_max + 1 : len;               // no row sees this or beyond
+    const int tiles_all = top_slot > 0 ? (top_slot + kTileKeys - 1) / kTileKeys : 0;
+    int jump = 0;                                                               // tiles cut out after the first tokens'
+    if (a.window > 0 && tile_min >= a.window) {
+        jump = (tile_min - a.window + 1) / kTileKeys - a.sink_tiles;
+        jump = jump > 0 ? jump : 0;
+    }
+    const int count = tiles_all - jump;
+    const int begin = part * a.chunk, end = count < begin + a.chunk ? count : begin + a.chunk;
+    auto slot_of = [&](int u) { return (u < a.sink_tiles ? u : u + jump) * kTileKeys; };
+
+    // this lane's query row
+    const int r = 32 * wave + (lane & 31);
+    const bool there = r < rows;
+    const int token = token_of(there ? r : 0);
+    const int head = kv * a.group + (r + head_shift - (token - (int)token0) * a.group);
+    const int64_t row = row0 + token;
+    const int position = there ? position_of(r) : -1;
+    u32x4 query[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int d = 16 * s + 8 * half;
+        query[s] = u32x4{0, 0, 0, 0};
+        if (there && (EXACT || d < a.dim)) {
+            query[s] = *reinterpret_cast<const u32x4*>(a.q + row * a.q_stride + (int64_t)head * a.dim + d);
+            query[s] = (query[s] & a.keep) ^ a.flip;
+        }
+    }
+
+    float m = -kInf, sum = 0.0f;
+    f32x16 acc[kBlocks];
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+        acc[k] = f32x16{};
+
+    // ---- loads: this lane's pieces of the wave's 16 rows
+    auto key_swizzle = [](int row) {
+        return DP == 64 ? (row >> 1) & 7 : DP == 96 ? (row >> 2) & 3 : row & 15;
+    };
+    auto value_swizzle = [](int row) {
+        return DP == 64 ? (row >> 1 & 1) << 2 : DP == 96 ? 0 : (row & 3) << 2;
+    };
+    const uint16_t* k0 = a.k + kv * a.at.stride_head;
+    const uint16_t* v0 = a.v + kv * a.at.stride_head;
+    int load_row[kLoads];
+    unsigned key_piece[kLoads], value_piece[kLoads];   // bytes from the row's start; WHOLE: from the 16 rows' start
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int p = i * 64 + lane, rw = p / CH, c = p - rw * CH;
+        const int kc = c ^ key_swizzle(rw), vc = c ^ value_swizzle(rw);
+        const unsigned first = WHOLE ? (unsigned)(rw * (int)a.at.stride_slot) * 2 : 0u;
+        load_row[i] = rw;
+        key_piece[i] = EXACT || kc * 8 < a.dim ? first + kc * 16 : kNowhere;
+        value_piece[i] = EXACT || vc * 8 < a.dim ? first + vc * 16 : kNowhere;
+    }
+    struct Place {
+        int page[WHOLE ? 1 : kLoads];
+    };
+    // the pages of step u, looked up a step before its loads
+    auto look = [&](int u) {
+        Place w;
+        const int j = slot_of(u) + 16 * wave;
+        if constexpr (WHOLE) {
+            w.page[0] = -1;
+            if (u < end && j < len)
+                w.page[0] = shared_word(a.at.table + b * a.at.table_stride + a.at.page_of.by(j));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                w.page[i] = -1;
+                if (u < end && j + load_row[i] < len)
+                    w.page[i] = a.at.table[b * a.at.table_stride + a.at.page_of.by(j + load_row[i])];
+            }
+        }
+        return w;
+    };
+    const unsigned wave_byte = __builtin_amdgcn_readfirstlane(lds_byte(&buffers[0][0][0])) + wave * 16 * CH * 16;
+    constexpr unsigned kHalfBytes = kTileKeys * CH * 16;
+    auto fetch = [&](int which, int u, const Place& w) {
+        const int j = slot_of(u) + 16 * wave;
+        const unsigned place_k = wave_byte + which * 2 * kHalfBytes, place_v = place_k + kHalfBytes;
+        unsigned bits;
+        if constexpr (WHOLE) {
+            const bool is = (unsigned)w.page[0] < (unsigned)a.at.pages;
+            const int left = is ? len - j : 0;
+            const int64_t at = is ? w.page[0] * a.at.stride_page + (int64_t)(j - a.at.page_of.by(j) * a.at.page_size) * a.at.stride_slot : 0;
+            const u32x4 keys = descriptor(k0 + at, is ? kNowhere - 1 : 0), values = descriptor(v0 + at, is ? kNowhere - 1 : 0);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                piece_to_lds(keys, load_row[i] < left ? key_piece[i] : kNowhere, place_k + i * 1024);
+                piece_to_lds(values, load_row[i] < left ? value_piece[i] : kNowhere, place_v + i * 1024);
+            }
+            bits = left >= 16 ? 0xFFFFu : (1u << (left > 0 ? left : 0)) - 1u;
+        } else {
+            bits = 0;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int s = j + load_row[i];
+                const bool is = s < len && (unsigned)w.page[i] < (unsigned)a.at.pages;
+                const int64_t at = is ? w.page[i] * a.at.stride_page + (int64_t)(s - a.at.page_of.by(s) * a.at.page_size) * a.at.stride_slot : 0;
+                const char* const ks = reinterpret_cast<const char*>(k0 + at), * const vs = reinterpret_cast<const char*>(v0 + at);
+                const char* const zeros = reinterpret_cast<const char*>(kZeros);
+                piece_to_lds(is && key_piece[i] != kNowhere ? ks + key_piece[i] : zeros, place_k + i * 1024);
+                piece_to_lds(is && value_piece[i] != kNowhere ? vs + value_piece[i] : zeros, place_v + i * 1024);
+                // a row's first piece speaks for it
+                const uint64_t lanes = __ballot(is);
+#pragma unroll
+                for (int rw = 0; rw < 16; ++rw)
+                    if (rw * CH >= i * 64 && rw * CH < i * 64 + 64)
+                        bits |= (unsigned)(lanes >> (rw * CH - i * 64) & 1) << rw;
+            }
+        }
+        if (lane == 0)
+            held_bits[which][wave] = (uint16_t)bits;
+    };
+
+    // ---- products
+    const int key_row = lane & 31;
+    const int key_base = key_swizzle(key_row & 15) ^ half;                       // piece 2 s + half lies at 2 s ^ key_base
+    const int i16 = lane & 15, value_row = 4 * half + (i16 >> 2);                // and 8, 16, ... rows on
+    const unsigned value_byte = (unsigned)(value_row * CH * 16 + (i16 & 1) * 8);
+    const int value_base = value_swizzle(value_row & 15);
+    const int value_col = 2 * (lane >> 4 & 1) + (i16 >> 1 & 1);                  // piece 4 block + this
+
+    auto key_piece_at = [&](int t, int e) { return (32 * t + key_row) * CH + ((2 * e) ^ key_base); };
+    // four and four keys of step `step` (16 keys), 32 columns from 32 `block` on
+    auto value = [&](const u32x4* values, int step, int block) {
+        const unsigned byte = value_byte + (unsigned)((4 * block + value_col) ^ value_base) * 16;
+        const u32x2 x = column_of_four(values, byte + (unsigned)(16 * step) * CH * 16);
+        const u32x2 y = column_of_four(values, byte + (unsigned)(16 * step + 8) * CH * 16);
+        return u32x4{x.x, x.y, y.x, y.y};
+    };
+    // the running maximum and all sums, where some logit passes it by kSlack
+    auto raise = [&](float top) {
+        if (__any(top > m + a.slack)) {
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float next = fmaxf(m, top);
+            const float f = m == -kInf ? 0.0f : exp2_hw((m - next) * a.scale);
+            m = next;
+            sum *= f;
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k)
+                acc[k] *= f;
+        }
+        return m == -kInf ? 0.0f : m * a.scale;
+    };
+    auto power_pair = [&](float x, float y, float ref) {
+        const unsigned pair = narrow_pair<DT>(exp2_hw(__builtin_fmaf(x, a.scale, -ref)), exp2_hw(__builtin_fmaf(y, a.scale, -ref)));
+        sum = add_pair<DT>(pair, sum);
+        return pair;
+    };
+
+    // a tile that every row sees whole
+    auto use = [&](const u32x4* keys, const u32x4* values) {
+        f32x16 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = f32x16{};
+#pragma unroll
+            for (int e = 0; e < kSteps; ++e)
+                s[t] = mfma_wide<DT>(keys[key_piece_at(t, e)], query[e], s[t]);
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i)
+            top = fmaxf(top, s[i / 16][i % 16]);
+        const float ref = raise(top);
+        u32x4 p[4];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+            p[i / 8][i % 8 / 2] = power_pair(s[i / 16][i % 16], s[i / 16][i % 16 + 1], ref);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k)
+                acc[k] = mfma_wide<DT>(value(values, e, k), p[e], acc[k]);
+    };
+
+    // any other tile, 32 keys at a time
+    auto use_masked = [&](const u32x4* keys, const u32x4* values, uint64_t held, int j0) {
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t, keys += 32 * CH, values += 32 * CH, held >>= 32, j0 += 32) {
+            f32x16 s = f32x16{};
+#pragma unroll
+            for (int e = 0; e < kSteps; ++e)
+                s = mfma_wide<DT>(keys[key_piece_at(0, e)], query[e], s);
+            // bit j: this lane's row sees slot j0 + j
+            unsigned seen = bits_below((int64_t)position + 1 - j0);
+            if (a.window > 0)
+                seen &= ~bits_below((int64_t)position + 1 - a.window - j0) | bits_below((int64_t)a.sinks - j0);
+            const unsigned visible = seen & (unsigned)held;
+            seen = visible >> (4 * half);   // element i is bit 8 (i / 4) + i % 4
+            float top = -kInf;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[i] = seen >> (8 * (i / 4) + i % 4) & 1 ? s[i] : -kInf;
+                top = fmaxf(top, s[i]);
+            }
+            const float ref = raise(top);
+            u32x4 p[2];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+                p[i / 8][i % 8 / 2] = power_pair(s[i], s[i + 1], ref);
+            constexpr unsigned kExp = DT == kF16 ? 0x7C007C00u : 0x7F807F80u, kLow = DT == kF16 ? 0x04000400u : 0x00800080u;
+            unsigned over = 0;
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const u32x4 x = value(values, e, k);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        over |= (x[w] & kExp) + kLow;
+                }
+            if (!__any((over & 0x80008000u) != 0)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int k = 0; k < kBlocks; ++k)
+                        acc[k] = mfma_wide<DT>(value(values, e, k), p[e], acc[k]);
+                continue;
+            }
+            // one key at a time, kept by the rows that see it
+#pragma unroll 1
+            for (int c = 0; c < 32; ++c) {
+                const bool sees = visible >> c & 1;
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k) {
+                    f32x16 next = acc[k];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        u32x4 x = value(values, e, k), w = p[e];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int first = 16 * e + 8 * (i / 2) + 2 * (i % 2) + 4 * half;   // key of the pair's lower half
+                            const unsigned only = c == first ? 0xFFFFu : c == first + 1 ? 0xFFFF0000u : 0u;
+                            x[i] &= only;
+                            w[i] &= only;
+                        }
+                        next = mfma_wide<DT>(x, w, next);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[k][i] = sees ? next[i] : acc[k][i];
+                }
+            }
+        }
+    };
+
+    // All of this wave's reads of the current buffers are done and its pieces of
+    // the next ones in LDS; after the barrier every wave's are.
+    auto turn = [] {
+        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) and lgkmcnt(0)
+        __syncthreads();
+    };
+    auto held_of = [](const uint16_t* at) {
+        uint64_t h;
+        __builtin_memcpy(&h, at, sizeof h);
+        return (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(h >> 32)) << 32 |
+               (unsigned)__builtin_amdgcn_readfirstlane((int)h);
+    };
+    if (begin < end) {
+        Place next = look(begin);
+        fetch(0, begin, next);
+        next = look(begin + 1);
+        int u = begin, which = 0;
+        // the buffers of step u are there, and the loads of the next one on their way
+        auto step = [&] {
+            turn();
+            if (u + 1 < end)
+                fetch(which ^ 1, u + 1, next);
+            next = look(u + 2);
+        };
+        // every row of the workgroup sees all of step u
+        auto whole = [&] {
+            const int j0 = slot_of(u);
+            return j0 + kTileKeys - 1 <= tile_min &&
+                   (a.window == 0 || j0 > tile_max - a.window || j0 + kTileKeys - 1 < a.sinks) &&
+                   held_of(held_bits[which]) == ~0ull;
+        };
+        step();
+        for (;;) {
+            // most steps: a loop of its own, so that what the others need costs it no registers
+            while (whole()) {
+                if (mine)
+                    use(buffers[which][0], buffers[which][1]);
+                if (++u >= end)
+                    break;
+                which ^= 1;
+                step();
+            }
+            if (u >= end)
+                break;
+            const int j0 = slot_of(u);
+            const bool unseen = j0 > wave_max || (a.window > 0 && j0 >= a.sinks && j0 + kTileKeys - 1 <= wave_min - a.window);
+            if (mine && !unseen)
+                use_masked(buffers[which][0], buffers[which][1], held_of(held_bits[which]), j0);
+            if (++u >= end)
+                break;
+            which ^= 1;
+            step();
+        }
+    }
+
+    sum += __shfl_xor(sum, 32);
+    if (!there)
+        return;
+    const int64_t at = row * a.q_heads + head;
+    if (a.part_out != nullptr) {
+        const int64_t to_part = at * a.parts + part;
+        if (half == 0) {
+            a.part_ms[to_part * 2] = m == -kInf ? -kInf : m * a.scale;
+            a.part_ms[to_part * 2 + 1] = sum;
+        }
+        if (begin < end)
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int d = 32 * k + 8 * i + 4 * half;
+                    if (EXACT || d < a.dim)
+                        *reinterpret_cast<f32x4*>(a.part_out + to_part * a.dim + d) =
+                            f32x4{acc[k][4 * i], acc[k][4 * i + 1], acc[k][4 * i + 2], acc[k][4 * i + 3]};
+                }
+        return;
+    }
+    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t* const out = static_cast<uint16_t*>(a.out) + at * a.dim;
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = 32 * k + 8 * i + 4 * half;
+            u32x2 w = {0, 0};
+            if (sum != 0.0f) {
+                w.x = narrow_pair<DT>(acc[k][4 * i] * by, acc[k][4 * i + 1] * by);
+                w.y = narrow_pair<DT>(acc[k][4 * i + 2] * by, acc[k][4 * i + 3] * by);
+            }
+            if (EXACT || d < a.dim)
+                *reinterpret_cast<u32x2*>(out + d) = w;
+        }
+}
+
+// Parts of the same rows: of `parts` each, in the layout of part_out and
+// part_ms.  `starts`: the groups whose rows the parts are of (a row outside
+// them has none), or null: every row.
+struct Source {
+    const float* ms;
+    const float* out;
+    int parts;
+    const int32_t* starts;
+    int batch;
+};
+
+struct Join {
+    Source from[2];
+    int rows, q_heads, dim;
+    const int32_t* starts;   // rows to write: the last max_new of each sequence; null: every row
+    int batch, max_new;
+    void* out;
+};
+
+// The sequence that holds a row, as [first, last) of its rows; false where none does.
+__device__ __forceinline__ bool sequence_of(const int32_t* starts, int batch, int rows, int64_t row, int64_t* first,
+                                            int64_t* last)
+{
+    const int lane = threadIdx.x & 63;
+    int low = 0, count = batch;
+    while (count > 1) {
+        const int step = (count + 63) / 64;
+        const int at = lane * step;
+        const int n = __popcll(__ballot(at < count && row_start(starts, low + at, rows) <= row));
+        const int skip = n > 0 ? (n - 1) * step : 0;
+        low += skip;
+        count = count - skip < step ? count - skip : step;
+    }
+    *first = row_start(starts, low, rows);
+    *last = row_start(starts, low + 1, rows);
+    return row >= *first && row < *last;
+}
+
+// A wave joins the parts of one row's head, in order: lanes take four elements
+// each, and parts in turn where a row needs fewer lanes than a wave has.
+template <int DT>
+__global__ void __launch_bounds__(256)
+join_parts_kernel(Join a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (at >= (int64_t)a.rows * a.q_heads)
+        return;
+    const int64_t row = at / a.q_heads;
+    int64_t first = 0, last = 0;
+    if (a.starts != nullptr && (!sequence_of(a.starts, a.batch, a.rows, row, &first, &last) || row < last - a.max_new))
+        return;
+    int parts[2];
+    float top = -kInf;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const Source& f = a.from[s];
+        parts[s] = f.parts;
+        if (f.parts > 0 && f.starts != nullptr && !sequence_of(f.starts, f.batch, a.rows, row, &first, &last))
+            parts[s] = 0;
+        for (int p = lane; p < parts[s]; p += 64)
+            top = fmaxf(top, f.ms[(at * f.parts + p) * 2]);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        top = fmaxf(top, __shfl_xor(top, d));
+    float total = 0.0f;
+    const int quads = a.dim >> 2;                       // lanes that a row needs: at most 64
+    const int ways = quads <= 8 ? 8 : quads <= 16 ? 4 : quads <= 32 ? 2 : 1;
+    const int lanes = 64 / ways, way = lane / lanes, d = lane - way * lanes;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const Source& f = a.from[s];
+#pragma unroll 4
+        for (int p = way; p < parts[s]; p += ways) {
+            const float pm = f.ms[(at * f.parts + p) * 2], ps = f.ms[(at * f.parts + p) * 2 + 1];
+            if (ps == 0.0f)
+                continue;                               // nothing seen: its sums were not written
+            const float w = part_factor(pm, ps, top);
+            total += w * ps;
+            if (d < quads)
+                o += w * *reinterpret_cast<const f32x4*>(f.out + (at * f.parts + p) * a.dim + 4 * d);
+        }
+    }
+    for (int w = lanes; w < 64; w <<= 1) {
+        total += __shfl_xor(total, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] += __shfl_xor(o[i], w);
+    }
+    if (way == 0 && d < quads) {
+        u32x2 w = {0, 0};
+        if (total != 0.0f) {
+            w.x = narrow_pair<DT>(o[0] / total, o[1] / total);
+            w.y = narrow_pair<DT>(o[2] / total, o[3] / total);
+        }
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * a.dim + 4 * d) = w;
+    }
+}
+
+}  // namespace gattn
