@@ -1,5 +1,6 @@
 """Row-major GEMV, y[M] = A[M,N] . x[N], on MI355X (gfx950), with the INT8
-product of several tokens and attention over a paged key-value cache.
+product of several tokens, attention over a paged key-value cache, and what
+stands between them.
 
 The compute lives in a hand-written HIP library behind a C ABI
 (``include/*.h``); ``binding`` is a thin ctypes layer over it.  The
@@ -27,4 +28,8 @@ from .binding import (  # noqa: F401,E402  (no library load at import time)
     prefix_attention,
     kv_append,
     kv_evict,
+    norm_rotate,
+    norm_rotate_append,
+    reserve_pages,
+    release_pages,
 )

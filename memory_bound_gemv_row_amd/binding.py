@@ -58,6 +58,25 @@ class KvBatch(ctypes.Structure):
                 ("lens", ctypes.c_void_p), ("batch", ctypes.c_int), ("max_len", ctypes.c_int)]
 
 
+class Rotation(ctypes.Structure):
+    """gemv_rotation: how heads are normed and rotated."""
+    _fields_ = [("head_dim", ctypes.c_int), ("rotated", ctypes.c_int), ("interleaved", ctypes.c_int), ("freqs", ctypes.c_void_p),
+                ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("weight_dtype", ctypes.c_int)]
+
+
+class Heads(ctypes.Structure):
+    """gemv_heads: the heads of a call's tokens."""
+    _fields_ = [("x", ctypes.c_void_p), ("stride", ctypes.c_int64), ("heads", ctypes.c_int), ("weight", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64)]
+
+
+class Pool(ctypes.Structure):
+    """gemv_page_pool: free pages, and the tables of the sequences that hold the others."""
+    _fields_ = [("free_pages", ctypes.c_void_p), ("count", ctypes.c_void_p), ("pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("width", ctypes.c_int), ("batch", ctypes.c_int)]
+
+
 def load():
     """Load the in-tree library (raises if it has not been built)."""
     global _lib
@@ -121,6 +140,17 @@ def load():
         lib.gemv_prefix_attention_workspace.restype = z
         lib.gemv_prefix_attention.argtypes = [cache, batch, p, batch, p, i64, i, f32, p, p, z, p]
         lib.gemv_prefix_attention.restype = i
+        turn, heads, pool = ctypes.POINTER(Rotation), ctypes.POINTER(Heads), ctypes.POINTER(Pool)
+        lib.gemv_norm_rotate.argtypes = [turn, heads, heads, i, i, p, i, p]
+        lib.gemv_norm_rotate.restype = i
+        lib.gemv_norm_rotate_append.argtypes = [turn, heads, heads, heads, i, p, i, cache, p, p]
+        lib.gemv_norm_rotate_append.restype = i
+        lib.gemv_reserve_pages.argtypes = [pool, p, p, i, p, p, p, p, p, p]
+        lib.gemv_reserve_pages.restype = i
+        lib.gemv_release_pages_workspace.argtypes = [pool]
+        lib.gemv_release_pages_workspace.restype = z
+        lib.gemv_release_pages.argtypes = [pool, p, p, p, z, p]
+        lib.gemv_release_pages.restype = i
         _lib = lib
         return lib
 
@@ -834,3 +864,168 @@ def kv_evict(cache, table, lens, seen, weights, positions, budget, recent, max_l
     _check(lib.gemv_kv_evict(c, s, np, wp, pp, shape[2], budget, recent, *outs, work.data_ptr() if need else None, need,
                              handle), "gemv_kv_evict")
     return new_w, new_p, left
+
+
+# ---------------------------------------------------------------- between projections and attention
+def _turned(x, name, weight, dim, here, dtype):
+    """gemv_heads of x [rows, heads, head_dim], without its output."""
+    rows, heads, d = x.shape
+    if d != dim:
+        raise ValueError(f"{name}: head_dim {d} != {dim}")
+    at, stride = _rows(x, name, dtype, (rows, heads, d), here, heads * d)
+    return Heads(at, stride, heads, None if weight is None else _ptr(weight, name + "_weight", weight.dtype, (d,), here), None,
+                 heads * d)
+
+
+def _rotation(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, here):
+    """(gemv_rotation, gemv_heads of q and of k, address of positions, rows) of a call."""
+    import torch
+
+    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0]:
+        raise ValueError("q and k must be [rows, heads, head_dim], of the same rows")
+    rows, heads, dim = q.shape
+    _dims(rows, heads, dim)
+    rotated = 2 * freqs.shape[0]
+    if freqs.dim() != 1 or rotated > dim:
+        raise ValueError(f"freqs: shape {tuple(freqs.shape)}, at most {dim // 2} pairs in heads of {dim}")
+    wanted = {w.dtype for w in (q_weight, k_weight) if w is not None}
+    if len(wanted) > 1:
+        raise TypeError("q_weight and k_weight must be of one type")
+    if wanted and eps is None:
+        raise ValueError("weights belong to a norm: eps is None")
+    how = Rotation(dim, rotated, bool(interleaved), _ptr(freqs, "freqs", torch.float64, (rotated // 2,), here), eps is not None,
+                   0.0 if eps is None else eps, _code(wanted.pop()) if wanted else 0)
+    return (how, _turned(q, "q", q_weight, dim, here, q.dtype), _turned(k, "k", k_weight, dim, here, q.dtype),
+            _ptr(positions, "positions", torch.int32, (rows,), here), rows)
+
+
+def norm_rotate(q, k, positions, freqs, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None, out_dtype=None,
+                stream=None):
+    """Norms the heads of q [rows, q_heads, head_dim] and k [rows, kv_heads,
+    head_dim] (float32, float16 or bfloat16, one type; rows may lie apart, as
+    parts of one product do) by their root mean square, times a weight
+    [head_dim], and rotates the first 2 * len(freqs) elements of each by the
+    angles positions[row] * freqs (positions int32 [rows], freqs float64,
+    radians): pairs (i, i + len(freqs)), or (2 i, 2 i + 1) if interleaved.
+    eps None leaves the norm out.  Returns (q, k) of `out_dtype` (q's unless
+    given), or writes them to ``out``, whose rows may lie apart too and which may
+    be q and k themselves."""
+    import torch
+
+    here = _here()
+    how, qh, kh, at, rows = _rotation(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, here)
+    handle, empty = _work_stream(stream, here)
+    if out is None:
+        out_dtype = out_dtype or q.dtype
+        code = _code(out_dtype)
+        out = empty(q.shape, dtype=out_dtype, device=q.device), empty(k.shape, dtype=out_dtype, device=q.device)
+        qh.out, kh.out = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        dtype = out[0].dtype
+        if out_dtype is not None and dtype != out_dtype:
+            raise TypeError(f"out is {dtype}, out_dtype {out_dtype}")
+        code = _code(dtype)
+        qh.out, qh.out_stride = _rows(out[0], "out[0]", dtype, tuple(q.shape), here, qh.heads * how.head_dim)
+        kh.out, kh.out_stride = _rows(out[1], "out[1]", dtype, tuple(k.shape), here, kh.heads * how.head_dim)
+    _check(load().gemv_norm_rotate(ctypes.byref(how), ctypes.byref(qh), ctypes.byref(kh), _code(q.dtype), code, at, rows, handle),
+           "gemv_norm_rotate")
+    return out
+
+
+def norm_rotate_append(cache, slots, q, k, v, positions, freqs, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                       out=None, stream=None):
+    """norm_rotate with k's results, and v [rows, kv_heads, head_dim] as it is,
+    put into a paged cache: row r's to slot slots[r] (int64 [rows], as
+    reserve_pages counts them; a slot outside the cache, such as -1, is left
+    out, and none stands twice).  Returns q's results, of the cache's type."""
+    import torch
+
+    here = _here()
+    if cache.index != here:
+        raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{here}")
+    how, qh, kh, at, rows = _rotation(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, here)
+    if how.head_dim != cache.head_dim or kh.heads != cache.heads or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{rows}, {cache.heads}, {cache.head_dim}]")
+    vh = _turned(v, "v", None, how.head_dim, here, q.dtype)
+    sp = _ptr(slots, "slots", torch.int64, (rows,), here)
+    handle, empty = _work_stream(stream, here)
+    if out is None:
+        out = empty(q.shape, dtype=cache.dtype, device=cache.device)
+        qh.out = out.data_ptr()
+    else:
+        qh.out, qh.out_stride = _rows(out, "out", cache.dtype, tuple(q.shape), here, qh.heads * how.head_dim)
+    _check(load().gemv_norm_rotate_append(ctypes.byref(how), ctypes.byref(qh), ctypes.byref(kh), ctypes.byref(vh), _code(q.dtype),
+                                          at, rows, cache._by_ref, sp, handle), "gemv_norm_rotate_append")
+    return out
+
+
+# ---------------------------------------------------------------- pages
+def _pool(free, count, table, page_size, here):
+    import torch
+
+    pages, (B, width) = free.shape[0], table.shape
+    _dims(pages, page_size, B, width)
+    fp = _ptr(free, "free", torch.int32, (pages,), here)
+    cp = _ptr(count, "count", torch.int32, (2,), here)
+    tp, stride = _rows(table, "table", torch.int32, (B, width), here, width)
+    return Pool(fp, cp, pages, page_size, tp, stride, width, B)
+
+
+def reserve_pages(free, count, table, lens, added, page_size, rows, out=None, stream=None):
+    """Room for added[b] new tokens of each sequence b, of lens[b] so far (int32
+    [batch]): pages from the stack free[: count[0]] (free int32 [pages of the
+    pool], count int32 [2]) are written to the rows of table int32 [batch, pages
+    per sequence] behind those that hold lens[b]; -1 where the stack is empty.
+    `rows`: new tokens in all, or more (padding).  Returns, or writes to
+    ``out``, (count afterwards: free pages and those that were missing; lens
+    afterwards; starts int32 [batch + 1] of the sequences' rows; positions int32
+    and slots int64 [rows] of the tokens, -1 without a page, and 0 and -1 in the
+    padding)."""
+    import torch
+
+    here = _here()
+    pool = _pool(free, count, table, page_size, here)
+    B = pool.batch
+    lp = _ptr(lens, "lens", torch.int32, (B,), here)
+    ap = _ptr(added, "added", torch.int32, (B,), here)
+    _dims(rows)
+    shapes = (("count", torch.int32, 2), ("lens", torch.int32, B), ("starts", torch.int32, B + 1), ("positions", torch.int32, rows),
+              ("slots", torch.int64, rows))
+    handle, empty = _work_stream(stream, here)
+    if out is None:
+        slots = empty(rows, dtype=torch.int64, device=free.device)
+        rest = empty(3 + 2 * B + rows, dtype=torch.int32, device=free.device)   # parts of one allocation
+        out = (*rest.split((2, B, B + 1, rows)), slots)
+        first = rest.data_ptr()
+        outs = first, first + 8, first + 8 + 4 * B, first + 12 + 8 * B, slots.data_ptr()
+    else:
+        outs = [_ptr(t, f"out[{i}]", dtype, (n,), here) for i, (t, (_, dtype, n)) in enumerate(zip(out, shapes, strict=True))]
+        size = [n * (8 if dtype is torch.int64 else 4) for _, dtype, n in shapes]
+        _apart(list(zip(outs, size)), [(lp, 4 * B), (ap, 4 * B), (pool.count, 8), (pool.free_pages, 4 * pool.pages),
+                                       (pool.table, 4 * ((B - 1) * pool.table_stride + pool.width) if B else 0)])
+    _check(load().gemv_reserve_pages(ctypes.byref(pool), lp, ap, rows, *outs, handle), "gemv_reserve_pages")
+    return out
+
+
+def release_pages(free, count, table, keep, page_size, out=None, stream=None):
+    """Gives back the pages that the rows of table hold past the first keep[b]
+    tokens of each sequence b (int32 [batch]; 0 releases it): they are put on the
+    stack free[: count[0]], and their entries become -1.  Such a page stands in
+    one row, once.  Returns, or writes to ``out``, the count afterwards."""
+    import torch
+
+    here = _here()
+    pool = _pool(free, count, table, page_size, here)
+    kp = _ptr(keep, "keep", torch.int32, (pool.batch,), here)
+    handle, empty = _work_stream(stream, here)
+    if out is None:
+        out = empty(2, dtype=torch.int32, device=free.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", torch.int32, (2,), here)
+        _apart([(op, 8)], [(pool.count, 8), (kp, 4 * pool.batch)])
+    lib, c = load(), ctypes.byref(pool)
+    need = lib.gemv_release_pages_workspace(c)
+    work = empty(need, dtype=torch.uint8, device=free.device) if need else None
+    _check(lib.gemv_release_pages(c, kp, op, work.data_ptr() if need else None, need, handle), "gemv_release_pages")
+    return out

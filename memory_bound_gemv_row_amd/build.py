@@ -5,9 +5,10 @@
 ``csrc/quant_api.hip`` (the weight quantiser), ``csrc/softmax_api.hip``
 (the row softmax), ``csrc/tokens_api.hip`` (the INT8 product of several
 tokens), ``csrc/attention_api.hip`` (attention over a paged key-value cache
-and the cache's upkeep) and ``csrc/prompt_api.hip`` (attention of several
-tokens, through a window and behind shared prefixes) into one library,
-``memory_bound_gemv_row_amd/libgemv_amd.so``.
+and the cache's upkeep), ``csrc/prompt_api.hip`` (attention of several tokens,
+through a window and behind shared prefixes), ``csrc/rotate_api.hip`` (norms
+and rotation of queries and keys) and ``csrc/pages_api.hip`` (pages for new
+tokens) into one library, ``memory_bound_gemv_row_amd/libgemv_amd.so``.
 """
 from __future__ import annotations
 
@@ -21,13 +22,15 @@ SRC_DIR = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemv_amd.so")
 SOURCES = [os.path.join(SRC_DIR, f) for f in ("gemv_api.hip", "quant_api.hip", "softmax_api.hip", "tokens_api.hip",
-                                                 "attention_api.hip", "prompt_api.hip")]
+                                                 "attention_api.hip", "prompt_api.hip", "rotate_api.hip",
+                                                 "pages_api.hip")]
 DEPENDS = SOURCES + [os.path.join(SRC_DIR, f) for f in ("gemv_kernels.hpp", "quant_kernels.hpp", "softmax_kernels.hpp",
                                                     "tokens_kernels.hpp", "paged.hpp", "attention_kernels.hpp",
-                                                    "cache_kernels.hpp", "prompt_kernels.hpp", "attention_host.hpp",
-                                                    "device_info.hpp")] \
+                                                    "cache_kernels.hpp", "prompt_kernels.hpp", "rotate_kernels.hpp",
+                                                    "pages_kernels.hpp", "attention_host.hpp", "device_info.hpp")] \
     + [os.path.join(INCLUDE, f) for f in ("gemv.h", "gemv_quant.h", "gemv_softmax.h", "gemv_types.h", "gemv_tokens.h",
-                                             "gemv_attention.h", "gemv_prompt.h")]
+                                             "gemv_attention.h", "gemv_prompt.h", "gemv_rotate.h",
+                                             "gemv_pages.h")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
