@@ -53,9 +53,8 @@ typedef struct gemv_heads {
 /* q and k of type `dtype` (gemv_dtype) -> their out of type `out_dtype`;
  * positions int32 [rows], negative ones too.  k may be NULL.  The outputs
  * overlap neither each other nor, but for the above, the inputs.
- * The bandwidth path needs 16-byte-aligned x, out and weights, strides and
- * head_dim that are multiples of 8, and rotated of 16 (of 8 where
- * interleaved); others go element by element.
+ * The bandwidth path needs 16-byte-aligned x, out and weights, and strides and
+ * head_dim that are multiples of 8; others go element by element.
  * GEMV_E_INVAL for negative sizes, a stride below heads * head_dim, rotated odd
  * or outside [0, head_dim], an unknown type or a missing pointer;
  * GEMV_E_UNSUPPORTED for head_dim over 256. */

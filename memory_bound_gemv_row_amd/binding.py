@@ -473,6 +473,23 @@ def _work_stream(stream, device):
     return stream.cuda_stream, empty
 
 
+def _like(t, dtype, empty):
+    """An empty dense tensor of t's shape and device; of its own type on the
+    current stream by the shorter of torch's calls."""
+    import torch
+
+    if empty is torch.empty and t.dtype is dtype:
+        return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+    return empty(t.shape, dtype=dtype, device=t.device)
+
+
+def _scratch(t, need, empty):
+    """`need` bytes of workspace on t's device, where t is of 16 bits."""
+    import torch
+
+    return t.new_empty((need + 1) // 2) if empty is torch.empty else empty(need, dtype=torch.uint8, device=t.device)
+
+
 def _ptr(t, name, dtype, shape, device):
     """Data pointer of a dense tensor of `dtype` and `shape` on `device`, the current one."""
     try:
@@ -489,8 +506,12 @@ def _rows(t, name, dtype, shape, device, dense):
     import torch
 
     try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
-            return t.data_ptr(), dense
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device:
+            if t.is_contiguous():
+                return t.data_ptr(), dense
+            stride = t.stride()
+            if len(stride) == 3 and stride[2] == 1 and stride[1] == shape[2] and stride[0] >= dense:
+                return t.data_ptr(), stride[0]
     except AttributeError:
         pass
     if not isinstance(t, torch.Tensor):
@@ -668,15 +689,13 @@ def _window(window, sinks):
 
 def _attend(cache, batch, room, starts, rows, max_new, q, scale, window, sinks, out, stream, here):
     """gemv_prompt_attention: `starts` is an address, or None for a row per sequence."""
-    import torch
-
-    heads, dim = q.shape[1], cache.head_dim
-    if q.shape[2] != dim or heads < 1 or heads % cache.heads:
-        raise ValueError(f"q: shape {tuple(q.shape)} does not fit {cache.heads} heads of {dim}")
+    _, heads, dim = q.shape
+    if dim != cache.head_dim or heads < 1 or heads % cache.heads:
+        raise ValueError(f"q: shape {tuple(q.shape)} does not fit {cache.heads} heads of {cache.head_dim}")
     qp, q_stride = _rows(q, "q", cache.dtype, (rows, heads, dim), here, heads * dim)
     handle, empty = _work_stream(stream, here)
     if out is None:
-        out = empty((rows, heads, dim), dtype=cache.dtype, device=cache.device)
+        out = _like(q, cache.dtype, empty)
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", cache.dtype, (rows, heads, dim), here)
@@ -684,7 +703,7 @@ def _attend(cache, batch, room, starts, rows, max_new, q, scale, window, sinks, 
     lib, c, s = load(), cache._by_ref, ctypes.byref(batch)
     need = cache._need(("rows", batch.batch, rows, max_new, heads, room, window, sinks),
                        lambda: lib.gemv_prompt_attention_workspace(c, s, rows, max_new, heads, window, sinks))
-    work = empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    work = _scratch(q, need, empty) if need else None
     _check(lib.gemv_prompt_attention(c, s, starts, rows, max_new, qp, q_stride, heads, scale, window, sinks, op,
                                      work.data_ptr() if need else None, need, handle), "gemv_prompt_attention")
     return out
@@ -782,7 +801,7 @@ def prefix_attention(cache, prefix_table, prefix_lens, starts, table, lens, q, s
     qp, q_stride = _rows(q, "q", cache.dtype, (B, heads, dim), here, heads * dim)
     handle, empty = _work_stream(stream, here)
     if out is None:
-        out = empty((B, heads, dim), dtype=cache.dtype, device=cache.device)
+        out = _like(q, cache.dtype, empty)
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", cache.dtype, (B, heads, dim), here)
@@ -790,7 +809,7 @@ def prefix_attention(cache, prefix_table, prefix_lens, starts, table, lens, q, s
     lib, c, f, s = load(), cache._by_ref, ctypes.byref(prefixes), ctypes.byref(batch)
     need = cache._need(("prefix", prefixes.batch, far, B, heads, room),
                        lambda: lib.gemv_prefix_attention_workspace(c, f, s, heads))
-    work = empty(need, dtype=torch.uint8, device=cache.device) if need else None
+    work = _scratch(q, need, empty) if need else None
     _check(lib.gemv_prefix_attention(c, f, sp, s, qp, q_stride, heads, scale, op, work.data_ptr() if need else None, need,
                                      handle), "gemv_prefix_attention")
     return out
@@ -867,35 +886,37 @@ def kv_evict(cache, table, lens, seen, weights, positions, budget, recent, max_l
 
 
 # ---------------------------------------------------------------- between projections and attention
-def _turned(x, name, weight, dim, here, dtype):
-    """gemv_heads of x [rows, heads, head_dim], without its output."""
-    rows, heads, d = x.shape
-    if d != dim:
-        raise ValueError(f"{name}: head_dim {d} != {dim}")
-    at, stride = _rows(x, name, dtype, (rows, heads, d), here, heads * d)
-    return Heads(at, stride, heads, None if weight is None else _ptr(weight, name + "_weight", weight.dtype, (d,), here), None,
-                 heads * d)
+def _turned(x, name, weight, rows, dim, here, dtype):
+    """gemv_heads of x [rows, heads, dim], without its output."""
+    r, heads, d = x.shape
+    if r != rows or d != dim:
+        raise ValueError(f"{name}: shape {tuple(x.shape)} is not [{rows}, heads, {dim}]")
+    width = heads * dim
+    at, stride = _rows(x, name, dtype, (rows, heads, dim), here, width)
+    return Heads(at, stride, heads, None if weight is None else _ptr(weight, name + "_weight", weight.dtype, (dim,), here), None, width)
 
 
 def _rotation(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, here):
     """(gemv_rotation, gemv_heads of q and of k, address of positions, rows) of a call."""
     import torch
 
-    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0]:
-        raise ValueError("q and k must be [rows, heads, head_dim], of the same rows")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, head_dim]")
     rows, heads, dim = q.shape
     _dims(rows, heads, dim)
-    rotated = 2 * freqs.shape[0]
-    if freqs.dim() != 1 or rotated > dim:
-        raise ValueError(f"freqs: shape {tuple(freqs.shape)}, at most {dim // 2} pairs in heads of {dim}")
-    wanted = {w.dtype for w in (q_weight, k_weight) if w is not None}
-    if len(wanted) > 1:
-        raise TypeError("q_weight and k_weight must be of one type")
-    if wanted and eps is None:
-        raise ValueError("weights belong to a norm: eps is None")
-    how = Rotation(dim, rotated, bool(interleaved), _ptr(freqs, "freqs", torch.float64, (rotated // 2,), here), eps is not None,
-                   0.0 if eps is None else eps, _code(wanted.pop()) if wanted else 0)
-    return (how, _turned(q, "q", q_weight, dim, here, q.dtype), _turned(k, "k", k_weight, dim, here, q.dtype),
+    half, = freqs.shape
+    if 2 * half > dim:
+        raise ValueError(f"freqs: {half} pairs do not fit in heads of {dim}")
+    weight = q_weight if q_weight is not None else k_weight
+    if weight is not None:
+        if k_weight is not None and k_weight.dtype is not weight.dtype:
+            raise TypeError("q_weight and k_weight must be of one type")
+        if eps is None:
+            raise ValueError("weights belong to a norm: eps is None")
+    dtype = q.dtype
+    return (Rotation(dim, 2 * half, bool(interleaved), _ptr(freqs, "freqs", torch.float64, (half,), here), eps is not None,
+                     0.0 if eps is None else eps, 0 if weight is None else _code(weight.dtype)),
+            _turned(q, "q", q_weight, rows, dim, here, dtype), _turned(k, "k", k_weight, rows, dim, here, dtype),
             _ptr(positions, "positions", torch.int32, (rows,), here), rows)
 
 
@@ -918,7 +939,7 @@ def norm_rotate(q, k, positions, freqs, q_weight=None, k_weight=None, eps=1e-6, 
     if out is None:
         out_dtype = out_dtype or q.dtype
         code = _code(out_dtype)
-        out = empty(q.shape, dtype=out_dtype, device=q.device), empty(k.shape, dtype=out_dtype, device=q.device)
+        out = _like(q, out_dtype, empty), _like(k, out_dtype, empty)
         qh.out, kh.out = out[0].data_ptr(), out[1].data_ptr()
     else:
         dtype = out[0].dtype
@@ -946,11 +967,11 @@ def norm_rotate_append(cache, slots, q, k, v, positions, freqs, q_weight=None, k
     how, qh, kh, at, rows = _rotation(q, k, positions, freqs, q_weight, k_weight, eps, interleaved, here)
     if how.head_dim != cache.head_dim or kh.heads != cache.heads or v.shape != k.shape:
         raise ValueError(f"k and v must be [{rows}, {cache.heads}, {cache.head_dim}]")
-    vh = _turned(v, "v", None, how.head_dim, here, q.dtype)
+    vh = _turned(v, "v", None, rows, how.head_dim, here, q.dtype)
     sp = _ptr(slots, "slots", torch.int64, (rows,), here)
     handle, empty = _work_stream(stream, here)
     if out is None:
-        out = empty(q.shape, dtype=cache.dtype, device=cache.device)
+        out = _like(q, cache.dtype, empty)
         qh.out = out.data_ptr()
     else:
         qh.out, qh.out_stride = _rows(out, "out", cache.dtype, tuple(q.shape), here, qh.heads * how.head_dim)
@@ -994,8 +1015,9 @@ def reserve_pages(free, count, table, lens, added, page_size, rows, out=None, st
     handle, empty = _work_stream(stream, here)
     if out is None:
         slots = empty(rows, dtype=torch.int64, device=free.device)
-        rest = empty(3 + 2 * B + rows, dtype=torch.int32, device=free.device)   # parts of one allocation
-        out = (*rest.split((2, B, B + 1, rows)), slots)
+        size = 3 + 2 * B + rows                                 # the others are parts of one allocation
+        rest = free.new_empty(size) if empty is torch.empty else empty(size, dtype=torch.int32, device=free.device)
+        out = (*rest.split_with_sizes((2, B, B + 1, rows)), slots)
         first = rest.data_ptr()
         outs = first, first + 8, first + 8 + 4 * B, first + 12 + 8 * B, slots.data_ptr()
     else:

@@ -22,12 +22,16 @@ struct Tiling {
     size_t ms_at, out_at, bytes;
 };
 
-// The least estimate, in tiles of keys, of what the busiest CU does: rounds of
-// two workgroups per CU (one for heads over 128), with `kStart` for a
-// workgroup's start and end and `kJoin` for a join.
-Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int limit, int window, int sinks, int cus)
+// The least estimate, in steps of a tile of keys: what the busiest of the places
+// for workgroups does (two per CU, one for heads over 128).  All the work spread
+// over the places, with `kStart` for a workgroup's start and end, and half of
+// the longest workgroup for an uneven end; or, where there is a place for each,
+// the longest one.  A join costs a launch, and the parts written and read: a step
+// takes about 2.3 us for heads of 128, in which memory moves 10 MB.
+Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int limit, int window, int sinks, int max_new,
+                 int cus)
 {
-    constexpr int kStart = 3, kJoin = 4;
+    constexpr double kStart = 3, kJoin = 2;
     Tiling t{};
     t.tiles = rows * group / kTileRows + batch;
     int64_t keys = ((int64_t)limit + kTileKeys - 1) / kTileKeys;
@@ -37,16 +41,21 @@ Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int
         keys = seen < keys ? seen : keys;
     }
     keys = keys > 0 ? keys : 1;
+    // of a sequence whose newest tokens are many, the first of them see fewer keys
+    const int64_t late = (int64_t)limit - max_new / 2;
+    const double mean = (double)keys < (double)late / kTileKeys + 1 ? (double)keys : (double)late / kTileKeys + 1;
     const int64_t each = (rows + batch - 1) / (batch > 0 ? batch : 1);   // new tokens of a sequence, about
-    const int64_t items = (int64_t)c->heads * batch * ((each * group + kTileRows - 1) / kTileRows);
-    const int64_t slots = (int64_t)cus * (c->head_dim > 128 ? 1 : 2);
-    int64_t least = INT64_MAX;
+    const double items = (double)c->heads * batch * (double)((each * group + kTileRows - 1) / kTileRows);
+    const double places = cus * (c->head_dim > 128 ? 1.0 : 2.0);
+    const double moved = (double)rows * group * c->heads * 8 * 128 / 10e6;   // in steps, for each part
+    double least = 0;
     for (int64_t parts = 1; parts <= keys && parts <= 256; ++parts) {
         const int64_t chunk = (keys + parts - 1) / parts;
         if ((keys + chunk - 1) / chunk != parts)
             continue;
-        const int64_t cost = (items * parts + slots - 1) / slots * (chunk + kStart) + (parts > 1 ? kJoin + parts / 16 : 0);
-        if (cost < least) {
+        const double all = items * (mean + kStart * parts) / places, longest = chunk + kStart;
+        const double cost = (items * parts <= places ? longest : all + longest / 2) + (parts > 1 ? kJoin + moved * parts : 0);
+        if (t.parts == 0 || cost < least) {
             least = cost;
             t.parts = (int)parts;
             t.chunk = (int)chunk;
@@ -132,15 +141,20 @@ const void* prompt_for(const gemv_kv_cache* c)
     return whole_tiles(c) ? prompt_sized<kBF16, true>(c->head_dim) : prompt_sized<kBF16, false>(c->head_dim);
 }
 
-int join_parts(const Join& j, int dtype, hipStream_t stream)
+// Few rows are joined by four waves each, where there are parts enough for them.
+int join_parts(const Join& j, int dtype, int cus, hipStream_t stream)
 {
     void* args[] = {(void*)&j};
-    const int64_t grid = ((int64_t)j.rows * j.q_heads + 3) / 4;
-    return launch(dtype == GEMV_F16 ? reinterpret_cast<const void*>(&join_parts_kernel<kF16>)
-                                    : reinterpret_cast<const void*>(&join_parts_kernel<kBF16>), grid, 256, args, stream);
+    const int64_t heads = (int64_t)j.rows * j.q_heads;
+    const bool spread = heads <= (int64_t)cus * 4 && j.from[0].parts + j.from[1].parts > 8;
+    const void* fn = dtype == GEMV_F16 ? spread ? reinterpret_cast<const void*>(&join_parts_kernel<kF16, true>)
+                                                : reinterpret_cast<const void*>(&join_parts_kernel<kF16, false>)
+                     : spread ? reinterpret_cast<const void*>(&join_parts_kernel<kBF16, true>)
+                              : reinterpret_cast<const void*>(&join_parts_kernel<kBF16, false>);
+    return launch(fn, spread ? heads : (heads + kJoinWaves - 1) / kJoinWaves, kJoinWaves * 64, args, stream);
 }
 
-bool joins_fit(int64_t rows, int q_heads) { return fits((rows * q_heads + 3) / 4, 256); }
+bool joins_fit(int64_t rows, int q_heads) { return fits((rows * q_heads + kJoinWaves - 1) / kJoinWaves, kJoinWaves * 64); }
 
 // Single new tokens, by the kernel of decode attention.  `at.limit` and
 // `split` are for the slots seen.
@@ -231,7 +245,8 @@ Plan plan_prompt(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int 
         p.bytes = p.joined ? p.out_at + (size_t)heads * p.split.parts * c->head_dim * sizeof(float) : 0;
         return p;
     }
-    p.tiling = tile_rows(c, rows, s->batch, q_heads / c->heads, limit, p.window, p.sinks, cus);
+    p.tiling = tile_rows(c, rows, s->batch, q_heads / c->heads, limit, p.window, p.sinks,
+                         max_new < rows ? max_new : rows, cus);
     p.joined = p.tiling.parts > 1;
     place_parts(&p.tiling, 0, heads, c->head_dim, p.joined);
     p.bytes = p.tiling.bytes;
@@ -249,7 +264,7 @@ PrefixPlan plan_prefix(const gemv_kv_cache* c, const gemv_kv_batch* prefixes, co
 {
     PrefixPlan p{};
     const int64_t heads = (int64_t)s->batch * q_heads;
-    p.shared = tile_rows(c, s->batch, prefixes->batch, q_heads / c->heads, far_limit, 0, 0, cus);
+    p.shared = tile_rows(c, s->batch, prefixes->batch, q_heads / c->heads, far_limit, 0, 0, 0, cus);
     if (prefixes->batch == 0 || far_limit == 0)
         p.shared.parts = 0;
     place_parts(&p.shared, 0, heads, c->head_dim, true);
@@ -345,7 +360,7 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
         if (int rc = launch(fn, grid, block, args, stream); rc != GEMV_OK || !p.joined)
             return rc;
         j.from[0] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
-        return join_parts(j, cache->dtype, stream);
+        return join_parts(j, cache->dtype, dev.cus, stream);
     }
     const int64_t grid = p.tiling.tiles * cache->heads * p.tiling.parts;
     if (!fits(grid, 256))
@@ -361,7 +376,7 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
     if (int rc = launch(prompt_for(cache), grid, 256, args, stream); rc != GEMV_OK || !p.joined)
         return rc;
     j.from[0] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
-    return join_parts(j, cache->dtype, stream);
+    return join_parts(j, cache->dtype, dev.cus, stream);
 }
 
 size_t gemv_prefix_attention_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* prefixes,
@@ -429,7 +444,7 @@ int gemv_prefix_attention(const gemv_kv_cache* cache, const gemv_kv_batch* prefi
             return rc;
         j.from[1] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
     }
-    return join_parts(j, cache->dtype, stream);
+    return join_parts(j, cache->dtype, dev.cus, stream);
 }
 
 }  // extern "C"

@@ -142,21 +142,33 @@ __device__ __forceinline__ unsigned bits_below(int64_t n) { return n <= 0 ? 0u :
 
 // The sequence whose row tiles hold place `u`, of places that a sequence b has
 // from floor(starts[b] * group / 128) + b on: as many as it can need, none
-// twice.  A wave looks at 64 sequences at a time.
-__device__ __forceinline__ int sequence_at(const int32_t* starts, int batch, int rows, int group, int64_t u)
+// twice.  A wave looks at 64 sequences at a time; what it has to know of the last
+// 64 is loaded at once, for each load that waits for another is half a
+// microsecond of a workgroup's start.
+struct Sequence {
+    int b, len;
+    int64_t from, to;   // its rows
+};
+
+__device__ __forceinline__ Sequence sequence_at(const Pages& at, const int32_t* starts, int batch, int rows, int group, int64_t u)
 {
     const int lane = threadIdx.x & 63;
     int low = 0, count = batch;   // the answer is in [low, low + count)
-    while (count > 1) {
+    while (count > 64) {
         const int step = (count + 63) / 64;
-        const int at = lane * step;
-        const bool below = at < count && row_start(starts, low + at, rows) * group / kTileRows + low + at <= u;
+        const int i = lane * step;
+        const bool below = i < count && row_start(starts, low + i, rows) * group / kTileRows + low + i <= u;
         const int n = __popcll(__ballot(below));   // the places rise with the sequence
         const int first = n > 0 ? (n - 1) * step : 0;
         low += first;
         count = count - first < step ? count - first : step;
     }
-    return low;
+    const int b = low + (lane < count ? lane : count - 1);
+    const int from = (int)row_start(starts, b, rows), to = (int)row_start(starts, b + 1, rows), len = at.length(b);
+    const int n = __popcll(__ballot(lane < count && (int64_t)from * group / kTileRows + b <= u));
+    const int it = n > 0 ? n - 1 : 0;
+    return Sequence{low + it, __builtin_amdgcn_readlane(len, it), __builtin_amdgcn_readlane(from, it),
+                    __builtin_amdgcn_readlane(to, it)};
 }
 
 // 16 zeros that slots without a page are read from
@@ -205,44 +217,50 @@ prompt_kernel(Prompt a)
 
     // Workgroups go to the eight XCDs in turn.  Those that read the same keys
     // (a head's, of a part) follow each other on one XCD where such sets are a
-    // multiple of eight; the last rows, which see most, come first.
+    // multiple of eight; the last rows, which see most, come first, and the last
+    // parts, which only long sequences have.  From part to part an XCD moves on by a head, so that it sees every head's part of the
+    // address space.
     const int sets = a.heads * a.parts;
+    // `one`: the same for all lanes, and known to be where the vector unit has computed it
+    auto one = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    auto quotient = [&](int x, int y) { return one((int)((unsigned)x / (unsigned)y)); };
     int set, place;
     if (sets % 8 == 0) {
-        const int j = (int)blockIdx.x >> 3, m = j / a.tiles;
+        const int j = (int)blockIdx.x >> 3, m = quotient(j, a.tiles);
         set = m * 8 + ((int)blockIdx.x & 7);
         place = j - m * a.tiles;
     } else {
-        place = (int)blockIdx.x / sets;
+        place = quotient((int)blockIdx.x, sets);
         set = (int)blockIdx.x - place * sets;
     }
-    const int kv = set % a.heads, part = set / a.heads;
+    const int part_back = quotient(set, a.heads), part = a.parts - 1 - part_back;
+    const int kv_at = set - part_back * a.heads + part;
+    const int kv = kv_at - quotient(kv_at, a.heads) * a.heads;
     place = a.tiles - 1 - place;
-    const int b = __builtin_amdgcn_readfirstlane(sequence_at(a.starts, a.batch, a.rows, a.group, place));
-    const int64_t from = row_start(a.starts, b, a.rows), to = row_start(a.starts, b + 1, a.rows);
+    const Sequence sequence = sequence_at(a.at, a.starts, a.batch, a.rows, a.group, place);
+    const int b = one(sequence.b), len = one(sequence.len);
+    const int64_t from = sequence.from, to = sequence.to;
     int64_t n64 = to - from;
     n64 = n64 < a.max_new ? n64 : a.max_new;
-    const int n = __builtin_amdgcn_readfirstlane((int)n64);                     // new tokens
+    const int n = one((int)n64);                     // new tokens
     const int64_t row0 = to - n64;                                              // the first of them
-    const int64_t r0 = (place - from * a.group / kTileRows - b) * kTileRows;   // this tile's first row
-    if (n <= 0 || r0 < 0 || r0 >= (int64_t)n * a.group)
+    // this tile's first row; rows times the group are below 2^30, as the launch's work-items are
+    const int r0 = one((int)(place - from * a.group / kTileRows - b) * kTileRows);
+    if (n <= 0 || r0 < 0 || r0 >= n * a.group)
         return;
-    const int len = __builtin_amdgcn_readfirstlane(a.at.length(b));
-    const int rows = (int)((int64_t)n * a.group - r0 < kTileRows ? (int64_t)n * a.group - r0 : kTileRows);
+    const int rows = n * a.group - r0 < kTileRows ? n * a.group - r0 : kTileRows;
 
     // tokens of the tile and of this wave, and the slots they see
-    const int64_t token0 = r0 / a.group;
-    const int head_shift = (int)(r0 - token0 * a.group);                        // r0 is head_shift rows past its token's first
-    auto token_of = [&](int r) { return (int)token0 + a.group_of.by(r + head_shift); };
+    auto token_of = [&](int r) { return a.group_of.by(r0 + r); };
     // position of a row's token, the last slot that it sees; -1: none
     auto position_of = [&](int r) {
         const int p = len - n + token_of(r);
         return !a.causal ? kEverySlot : p > -1 ? p : -1;
     };
-    const int tile_min = position_of(0), tile_max = position_of(rows - 1);
+    const int tile_min = one(position_of(0)), tile_max = one(position_of(rows - 1));
     const bool mine = 32 * wave < rows;
     const int last = rows - 1 < 32 * wave + 31 ? rows - 1 : 32 * wave + 31;
-    const int wave_min = position_of(mine ? 32 * wave : 0), wave_max = position_of(last);
+    const int wave_min = one(position_of(mine ? 32 * wave : 0)), wave_max = one(position_of(last));
     const int top_slot = tile_max + 1 < len ? tile_max + 1 : len;               // no row sees this or beyond
     const int tiles_all = top_slot > 0 ? (top_slot + kTileKeys - 1) / kTileKeys : 0;
     int jump = 0;                                                               // tiles cut out after the first tokens'
@@ -257,20 +275,13 @@ prompt_kernel(Prompt a)
     // this lane's query row
     const int r = 32 * wave + (lane & 31);
     const bool there = r < rows;
-    const int token = token_of(there ? r : 0);
-    const int head = kv * a.group + (r + head_shift - (token - (int)token0) * a.group);
+    const int safe = there ? r : 0;                                             // no lane's address needs a branch
+    const int token = token_of(safe);
+    const int head = kv * a.group + (r0 + safe - token * a.group);
     const int64_t row = row0 + token;
     const int position = there ? position_of(r) : -1;
-    u32x4 query[kSteps];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int d = 16 * s + 8 * half;
-        query[s] = u32x4{0, 0, 0, 0};
-        if (there && (EXACT || d < a.dim)) {
-            query[s] = *reinterpret_cast<const u32x4*>(a.q + row * a.q_stride + (int64_t)head * a.dim + d);
-            query[s] = (query[s] & a.keep) ^ a.flip;
-        }
-    }
+    u32x4 query[kSteps];   // loaded behind the first keys
+    const uint16_t* const query_at = a.q + row * a.q_stride + (int64_t)head * a.dim;
 
     float m = -kInf, sum = 0.0f;
     f32x16 acc[kBlocks];
@@ -508,6 +519,14 @@ prompt_kernel(Prompt a)
         Place next = look(begin);
         fetch(0, begin, next);
         next = look(begin + 1);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int d = 16 * s + 8 * half;
+            query[s] = *reinterpret_cast<const u32x4*>(query_at + (EXACT || d < a.dim ? d : 0));
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+            query[s] = there && (EXACT || 16 * s + 8 * half < a.dim) ? (query[s] & a.keep) ^ a.flip : u32x4{0, 0, 0, 0};
         int u = begin, which = 0;
         // the buffers of step u are there, and the loads of the next one on their way
         auto step = [&] {
@@ -624,14 +643,95 @@ __device__ __forceinline__ bool sequence_of(const int32_t* starts, int batch, in
     return row >= *first && row < *last;
 }
 
-// A wave joins the parts of one row's head, in order: lanes take four elements
-// each, and parts in turn where a row needs fewer lanes than a wave has.
-template <int DT>
-__global__ void __launch_bounds__(256)
+// WAVES waves join the parts of one row's head: parts 64 at a time, an eighth or a
+// quarter of those a wave where there are several, in a fixed order.  Lane p has
+// part p's maximum and sum, and so its weight; then every lane adds up its E
+// elements over the parts that saw anything, whose loads do not wait for each
+// other.
+template <int DT, int E, int WAVES>
+__device__ __forceinline__ void join_row(const Join& a, int64_t at, const int (&parts)[2])
+{
+    typedef float f32xE __attribute__((ext_vector_type(E)));
+    __shared__ float red_o[WAVES > 1 ? WAVES : 1][WAVES > 1 ? 64 * E : 1];
+    __shared__ float red_t[WAVES];
+    const int lane = threadIdx.x & 63;
+    const int wave = WAVES > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+    float top = -kInf;
+    for (int s = 0; s < 2; ++s)
+        for (int p = lane; p < parts[s]; p += 64)
+            top = fmaxf(top, a.from[s].ms[(at * a.from[s].parts + p) * 2]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        top = fmaxf(top, __shfl_xor(top, d));
+    const bool mine = lane * E < a.dim;
+    float total = 0.0f;
+    f32xE o = {};
+    for (int s = 0; s < 2; ++s) {
+        const Source& f = a.from[s];
+        for (int base = 0; base < parts[s]; base += 64) {
+            float w = 0.0f, ps = 0.0f;
+            if (base + lane < parts[s] && (WAVES == 1 || lane % WAVES == wave)) {
+                const float* ms = f.ms + (at * f.parts + base + lane) * 2;
+                ps = ms[1];
+                w = part_factor(ms[0], ps, top);
+            }
+            uint64_t live = __ballot(!(ps == 0.0f));    // the others saw nothing: their sums were not written
+            total += w * ps;
+            const float* out = f.out + (at * f.parts + base) * a.dim + lane * E;
+            while (live != 0) {
+                f32xE x[8];
+                float wp[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int p = live != 0 ? __builtin_ctzll(live) : 0;
+                    wp[i] = live != 0 ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), p)) : 0.0f;
+                    x[i] = f32xE{};
+                    if (live != 0 && mine)
+                        x[i] = *reinterpret_cast<const f32xE*>(out + (int64_t)p * a.dim);
+                    live &= live - 1;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o += wp[i] * x[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        total += __shfl_xor(total, d);
+    if constexpr (WAVES > 1) {
+        *reinterpret_cast<f32xE*>(&red_o[wave][lane * E]) = o;
+        if (lane == 0)
+            red_t[wave] = total;
+        __syncthreads();
+        if (wave > 0)
+            return;
+        for (int w = 1; w < WAVES; ++w) {
+            o += *reinterpret_cast<const f32xE*>(&red_o[w][lane * E]);
+            total += red_t[w];
+        }
+    }
+    if (!mine)
+        return;
+    uint16_t* const to = static_cast<uint16_t*>(a.out) + at * a.dim + lane * E;
+    if constexpr (E == 1) {
+        narrow_to<DT>(to, 0, total == 0.0f ? 0.0f : o[0] / total);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            reinterpret_cast<unsigned*>(to)[e / 2] = total == 0.0f ? 0u : narrow_pair<DT>(o[e] / total, o[e + 1] / total);
+    }
+}
+
+constexpr int kJoinWaves = 4;
+
+// A wave for each row's head, or (SPREAD) all four where there are few rows.
+template <int DT, bool SPREAD>
+__global__ void __launch_bounds__(kJoinWaves * 64)
 join_parts_kernel(Join a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t at = SPREAD ? (int64_t)blockIdx.x
+                              : (int64_t)blockIdx.x * kJoinWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (at >= (int64_t)a.rows * a.q_heads)
         return;
     const int64_t row = at / a.q_heads;
@@ -639,52 +739,20 @@ join_parts_kernel(Join a)
     if (a.starts != nullptr && (!sequence_of(a.starts, a.batch, a.rows, row, &first, &last) || row < last - a.max_new))
         return;
     int parts[2];
-    float top = -kInf;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const Source& f = a.from[s];
         parts[s] = f.parts;
         if (f.parts > 0 && f.starts != nullptr && !sequence_of(f.starts, f.batch, a.rows, row, &first, &last))
             parts[s] = 0;
-        for (int p = lane; p < parts[s]; p += 64)
-            top = fmaxf(top, f.ms[(at * f.parts + p) * 2]);
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        top = fmaxf(top, __shfl_xor(top, d));
-    float total = 0.0f;
-    const int quads = a.dim >> 2;                       // lanes that a row needs: at most 64
-    const int ways = quads <= 8 ? 8 : quads <= 16 ? 4 : quads <= 32 ? 2 : 1;
-    const int lanes = 64 / ways, way = lane / lanes, d = lane - way * lanes;
-    f32x4 o = {0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const Source& f = a.from[s];
-#pragma unroll 4
-        for (int p = way; p < parts[s]; p += ways) {
-            const float pm = f.ms[(at * f.parts + p) * 2], ps = f.ms[(at * f.parts + p) * 2 + 1];
-            if (ps == 0.0f)
-                continue;                               // nothing seen: its sums were not written
-            const float w = part_factor(pm, ps, top);
-            total += w * ps;
-            if (d < quads)
-                o += w * *reinterpret_cast<const f32x4*>(f.out + (at * f.parts + p) * a.dim + 4 * d);
-        }
-    }
-    for (int w = lanes; w < 64; w <<= 1) {
-        total += __shfl_xor(total, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] += __shfl_xor(o[i], w);
-    }
-    if (way == 0 && d < quads) {
-        u32x2 w = {0, 0};
-        if (total != 0.0f) {
-            w.x = narrow_pair<DT>(o[0] / total, o[1] / total);
-            w.y = narrow_pair<DT>(o[2] / total, o[3] / total);
-        }
-        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * a.dim + 4 * d) = w;
-    }
+    constexpr int W = SPREAD ? kJoinWaves : 1;
+    if (a.dim <= 64)
+        join_row<DT, 1, W>(a, at, parts);
+    else if (a.dim <= 128)
+        join_row<DT, 2, W>(a, at, parts);
+    else
+        join_row<DT, 4, W>(a, at, parts);
 }
 
 }  // namespace gattn

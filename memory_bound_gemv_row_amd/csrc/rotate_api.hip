@@ -37,18 +37,22 @@ bool wide(const gemv_heads* h, bool own_out)
            (!own_out || (aligned(h->out, 16) && h->out_stride % 8 == 0));
 }
 
+constexpr int kElements = -1;   // in the place of a pairing: element by element
+
 template <int IN, int OUT>
-const void* kernel_for(bool vector)
+const void* kernel_for(int pairing)
 {
-    return vector ? reinterpret_cast<const void*>(&rotate_kernel<IN, OUT>)
-                  : reinterpret_cast<const void*>(&rotate_elementwise<IN, OUT>);
+    return pairing == kHalves       ? reinterpret_cast<const void*>(&rotate_kernel<IN, OUT, kHalves>)
+           : pairing == kNeighbours ? reinterpret_cast<const void*>(&rotate_kernel<IN, OUT, kNeighbours>)
+           : pairing == kLoose      ? reinterpret_cast<const void*>(&rotate_kernel<IN, OUT, kLoose>)
+                                    : reinterpret_cast<const void*>(&rotate_elementwise<IN, OUT>);
 }
 
 template <int IN>
-const void* kernel_for(int out, bool vector)
+const void* kernel_for(int out, int pairing)
 {
-    return out == GEMV_F32 ? kernel_for<IN, kF32>(vector) : out == GEMV_F16 ? kernel_for<IN, kF16>(vector)
-                                                                            : kernel_for<IN, kBF16>(vector);
+    return out == GEMV_F32 ? kernel_for<IN, kF32>(pairing) : out == GEMV_F16 ? kernel_for<IN, kF16>(pairing)
+                                                                             : kernel_for<IN, kBF16>(pairing);
 }
 
 int run(Rotate& a, bool vector, int in, int out, hipStream_t stream)
@@ -56,10 +60,11 @@ int run(Rotate& a, bool vector, int in, int out, hipStream_t stream)
     gemv_device::Device dev{};
     if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
         return rc;
-    int per = 1;
+    int per = 1, pairing = kElements;
     if (vector) {
         const int half = a.rotated / 2;
-        a.units = a.interleaved ? (a.dim / 8 + 1) / 2 : half / 8 + ((a.dim - a.rotated) / 8 + 1) / 2;
+        pairing = a.interleaved ? kNeighbours : half % 8 == 0 ? kHalves : kLoose;
+        a.units = pairing == kHalves ? half / 8 + ((a.dim - a.rotated) / 8 + 1) / 2 : (a.dim / 8 + 1) / 2;
         a.lanes = 1;
         while (a.lanes < a.units)
             a.lanes *= 2;
@@ -70,12 +75,16 @@ int run(Rotate& a, bool vector, int in, int out, hipStream_t stream)
     a.turns = a.of[0].turns + a.of[1].turns + a.of[2].turns;
     if (a.turns == 0 || a.rows == 0)
         return GEMV_OK;
-    // a wave takes more than one step of its row only where the card is full of waves without
-    const int64_t steps = (int64_t)a.rows * a.turns, full = (int64_t)dev.cus * 32;
-    a.span = vector ? (int)(steps / full < 1 ? 1 : steps / full < a.turns ? steps / full : a.turns) : 1;
+    // a row's steps are shared out among waves only until there are about twelve a CU:
+    // its angles are taken by each of them (8191 rows of 32 + 8 + 8 heads of 128, six
+    // steps: 46.9 us by one wave, 55.2 by three; 1000 rows: 14.0 and 9.0); element by
+    // element the waves wait more
+    const int64_t full = (int64_t)dev.cus * (vector ? 12 : 64), share = (full + a.rows / 2) / a.rows;
+    const int spans_of = (int)(share < 1 ? 1 : share < a.turns ? share : a.turns);
+    a.span = (a.turns + spans_of - 1) / spans_of;
     const int64_t waves = (int64_t)a.rows * ((a.turns + a.span - 1) / a.span);
-    const void* fn = in == GEMV_F32   ? kernel_for<kF32>(out, vector)
-                     : in == GEMV_F16 ? kernel_for<kF16>(out, vector) : kernel_for<kBF16>(out, vector);
+    const void* fn = in == GEMV_F32   ? kernel_for<kF32>(out, pairing)
+                     : in == GEMV_F16 ? kernel_for<kF16>(out, pairing) : kernel_for<kBF16>(out, pairing);
     void* args[] = {(void*)&a};
     const int grid = gemv_device::capped_grid((waves + kWaves - 1) / kWaves, kWaves * 64);
     return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(kWaves * 64), args, 0, stream) == hipSuccess ? GEMV_OK : GEMV_E_LAUNCH;
@@ -93,6 +102,7 @@ Rotate rotation_of(const gemv_rotation* how, const int32_t* positions, int rows)
     a.rows = rows;
     a.dim = how->head_dim;
     a.rotated = how->rotated;
+    a.per_element = 1.0f / (float)how->head_dim;
     a.interleaved = how->interleaved != 0;
     a.norm = how->norm != 0;
     a.eps = how->eps;
@@ -101,7 +111,7 @@ Rotate rotation_of(const gemv_rotation* how, const int32_t* positions, int rows)
     return a;
 }
 
-bool pieces(const gemv_rotation* how) { return how->head_dim % 8 == 0 && how->rotated % (how->interleaved ? 8 : 16) == 0; }
+bool pieces(const gemv_rotation* how) { return how->head_dim % 8 == 0; }
 
 }  // namespace
 }  // namespace grot

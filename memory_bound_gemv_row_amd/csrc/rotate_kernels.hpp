@@ -39,6 +39,10 @@ struct Elem<kBF16> {
 constexpr int kMaxDim = 256;
 constexpr int kWaves = 4;
 
+// How the pairs of a head lie to the pieces of eight elements: halves of whole
+// pieces, neighbours, and halves that end inside a piece.
+enum Pairing : int { kHalves = 0, kNeighbours = 1, kLoose = 2 };
+
 enum Kind : int { kQuery = 0, kKey = 1, kValue = 2 };
 
 struct Heads {
@@ -55,6 +59,7 @@ struct Rotate {
     Heads of[3];             // queries, keys, values
     const int32_t* positions;
     int rows, dim, rotated;
+    float per_element;       // 1 / dim
     bool interleaved, norm;
     float eps;
     const double* freqs;
@@ -96,6 +101,16 @@ __device__ __forceinline__ float group_sum(float v, int lanes)
     if (lanes > 8)
         v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x140, 0xF, 0xF, true));   // 16 lanes mirrored
     return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+    const int s = __builtin_bit_cast(int, group_sum(v, 16));
+    float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 64; i += 16)
+        total += __builtin_bit_cast(float, __builtin_amdgcn_readlane(s, i));
+    return total;
 }
 
 __device__ __forceinline__ float weight_at(const void* w, int dtype, int d)
@@ -147,18 +162,24 @@ __device__ __forceinline__ int kind_at(const Rotate& a, int turn, int per, int* 
 }
 
 // A wave per row (or per `span` of its steps where there are few rows).  A lane
-// holds two pieces of eight elements of a head, such that its pairs are its own:
-// the pieces at 8 u and rotated / 2 + 8 u, or at 16 u and 16 u + 8 where pairs
-// are neighbours; both times its angles are 8 u .. 8 u + 7.  A head takes 1 to
-// 16 lanes, a step 64 / lanes heads of a kind.  The angles of a row are taken
-// once, one a lane, and meet the heads over LDS.
-template <int IN, int OUT>
+// holds two pieces of eight elements of a head.  With halves of whole pieces
+// they are those at 8 u and rotated / 2 + 8 u, with neighbours as pairs those at
+// 16 u and 16 u + 8: a lane's pairs are its own, and both times its angles are
+// 8 u .. 8 u + 7.  Loose halves are held like neighbours, and each element's other
+// half comes over LDS.  A head takes 1 to 16 lanes, a step 64 / lanes heads of a
+// kind.  The angles of a row are taken once, one a lane, and meet the heads over
+// LDS.
+//
+// 8191 tokens of 32 + 8 + 8 heads of 128 (bfloat16) into a cache: 43.5 us, 4.6
+// TB/s read and written, where a copy makes 4.95; one token 3.7 us.
+template <int IN, int OUT, int PAIRING>
 __global__ void __launch_bounds__(kWaves * 64)
 rotate_kernel(Rotate a)
 {
     typedef typename Elem<IN>::wide In;
     typedef typename Elem<OUT>::wide Out;
     __shared__ __attribute__((aligned(16))) float cosines[kWaves][kMaxDim / 2], sines[kWaves][kMaxDim / 2];
+    __shared__ __attribute__((aligned(16))) float others[PAIRING == kLoose ? kWaves : 1][PAIRING == kLoose ? 64 * 16 : 1];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int spans = (a.turns + a.span - 1) / a.span;
@@ -167,23 +188,14 @@ rotate_kernel(Rotate a)
     const int group = lane / a.lanes, unit = lane - group * a.lanes;
     const bool live = unit < a.units;
 
-    // this lane's two pieces: elements first and second on, with angles or without
-    int first, second;
-    bool turned, second_turned;
+    // this lane's two pieces: elements first and second on
     const int half = a.rotated / 2;
-    if (a.interleaved) {
-        first = 16 * unit;
-        second = first + 8;
-        turned = first < a.rotated;
-        second_turned = second < a.rotated;
-    } else if (8 * unit < half) {
-        first = 8 * unit;
-        second = half + first;
-        turned = second_turned = true;
-    } else {
-        first = a.rotated + 16 * (unit - half / 8);
-        second = first + 8;
-        turned = second_turned = false;
+    int first = 16 * unit, second = first + 8;
+    bool turned = PAIRING == kNeighbours && first < a.rotated;
+    if constexpr (PAIRING == kHalves) {
+        turned = 8 * unit < half;
+        first = turned ? 8 * unit : a.rotated + 16 * (unit - half / 8);
+        second = turned ? half + first : first + 8;
     }
     const bool both = live && second < a.dim;
 
@@ -193,31 +205,42 @@ rotate_kernel(Rotate a)
         const int64_t row = spans == 1 ? item : item / spans;
         const int begin = (int)(item - row * spans) * a.span, end = begin + a.span < a.turns ? begin + a.span : a.turns;
         // a step's pieces are loaded while the step before is turned, the first ones behind the angles
-        auto load = [&](int turn, f32x8& x, f32x8& y) {
+        auto load = [&](int turn, In& x, In& y) {
             int head;
             const int kind = __builtin_amdgcn_readfirstlane(kind_at(a, turn, per, &head));
             head += group;
             const Heads& h = a.of[kind];
             const typename Elem<IN>::type* from = static_cast<const typename Elem<IN>::type*>(h.x) + row * h.stride + (int64_t)head * a.dim;
-            x = y = f32x8{};
+            x = y = In{};
             if (live && head < h.heads)
-                x = __builtin_convertvector(*reinterpret_cast<const In*>(from + first), f32x8);
+                x = *reinterpret_cast<const In*>(from + first);
             if (both && head < h.heads)
-                y = __builtin_convertvector(*reinterpret_cast<const In*>(from + second), f32x8);
+                y = *reinterpret_cast<const In*>(from + second);
         };
-        f32x8 x, y, next_x = {}, next_y = {};
-        load(begin, x, y);
+        In next_x, next_y;
+        load(begin, next_x, next_y);
         const int position = a.positions[row];
         for (int i = lane; i < half; i += 64) {
             const float2 t = turn_of(position, a.freqs[i]);
             cosines[wave][i] = t.x;
             sines[wave][i] = t.y;
         }
-        // a wave reads what it wrote itself: its writes are done once they are waited for
+        // a wave reads what it wrote itself, and LDS takes its accesses in order
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        f32x8 c = {}, s = {};
-        if (live && turned) {
+        f32x8 c = {}, s = {}, c_second = {}, s_second = {};
+        int other[PAIRING == kLoose ? 16 : 1];   // where each element's other half lies among the lane's head's
+        if constexpr (PAIRING == kLoose) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int d = first + e, pair = d < half ? d : d - half;
+                const bool is = d < a.rotated;
+                other[e] = !is ? d : d < half ? d + half : d - half;
+                const float cosine = is ? cosines[wave][pair] : 1.0f, sine = is ? sines[wave][pair] : 0.0f;
+                (e < 8 ? c : c_second)[e & 7] = cosine;
+                (e < 8 ? s : s_second)[e & 7] = d < half ? -sine : sine;
+            }
+        } else if (live && turned) {
             c = *reinterpret_cast<const f32x8*>(&cosines[wave][8 * unit]);
             s = *reinterpret_cast<const f32x8*>(&sines[wave][8 * unit]);
         }
@@ -227,6 +250,7 @@ rotate_kernel(Rotate a)
             head += group;
             const Heads& h = a.of[kind];
             const bool mine = live && head < h.heads, mine_too = both && head < h.heads;
+            f32x8 x = __builtin_convertvector(next_x, f32x8), y = __builtin_convertvector(next_y, f32x8);
             if (turn + 1 < end)
                 load(turn + 1, next_x, next_y);
             if (kind != kValue) {
@@ -244,28 +268,43 @@ rotate_kernel(Rotate a)
                     for (int e = 0; e < 8; ++e)
                         sum += x[e] * x[e] + y[e] * y[e];
                     sum = group_sum(sum, a.lanes);
-                    const float by = __builtin_amdgcn_rsqf(sum / (float)a.dim + a.eps);
+                    const float by = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, a.per_element, a.eps));
                     x = x * by * weight_first;
                     y = y * by * weight_second;
                 }
-                if (a.interleaved) {
+                if constexpr (PAIRING == kNeighbours) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (turned) {
+                        if (first + 2 * e < a.rotated) {
                             const float p = x[2 * e], q = x[2 * e + 1];
                             x[2 * e] = p * c[e] - q * s[e];
                             x[2 * e + 1] = q * c[e] + p * s[e];
                         }
-                        if (second_turned) {
+                        if (second + 2 * e < a.rotated) {
                             const float p = y[2 * e], q = y[2 * e + 1];
                             y[2 * e] = p * c[4 + e] - q * s[4 + e];
                             y[2 * e + 1] = q * c[4 + e] + p * s[4 + e];
                         }
                     }
-                } else if (turned) {
-                    const f32x8 p = x, q = y;
-                    x = p * c - q * s;
-                    y = q * c + p * s;
+                } else if constexpr (PAIRING == kHalves) {
+                    if (turned) {
+                        const f32x8 p = x, q = y;
+                        x = p * c - q * s;
+                        y = q * c + p * s;
+                    }
+                } else {
+                    float* const mine_all = &others[wave][group * a.lanes * 16];
+                    *reinterpret_cast<f32x8*>(&mine_all[first]) = x;
+                    *reinterpret_cast<f32x8*>(&mine_all[second]) = y;
+                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float p = mine_all[other[e]], q = mine_all[other[8 + e]];
+                        x[e] = first + e < a.rotated ? x[e] * c[e] + p * s[e] : x[e];
+                        y[e] = second + e < a.rotated ? y[e] * c_second[e] + q * s_second[e] : y[e];
+                    }
+                    __builtin_amdgcn_wave_barrier();   // the next step's writes come after these reads
                 }
             }
             int64_t head_stride;
@@ -277,15 +316,14 @@ rotate_kernel(Rotate a)
                 if (mine_too)
                     *reinterpret_cast<Out*>(to + second) = __builtin_convertvector(y, Out);
             }
-            x = next_x;
-            y = next_y;
         }
         __builtin_amdgcn_wave_barrier();   // the next row's angles come after this row's reads
     }
 }
 
-// Any size and alignment: a wave per head, a pair (or an element past the
-// rotated ones) a lane at a time.
+// Any size and alignment: a wave takes one head after the other, a pair (or an
+// element past the rotated ones) a lane at a time, so that a lane's angles are
+// those of every head of the row.
 template <int IN, int OUT>
 __global__ void __launch_bounds__(kWaves * 64)
 rotate_elementwise(Rotate a)
@@ -294,70 +332,98 @@ rotate_elementwise(Rotate a)
     typedef typename Elem<OUT>::type O;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int spans = (a.turns + a.span - 1) / a.span;
+    const int64_t items = (int64_t)a.rows * spans;
     const int half = a.rotated / 2, singles = a.dim - a.rotated;
-    for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < (int64_t)a.rows * a.turns; item += (int64_t)gridDim.x * kWaves) {
-        const int64_t row = item / a.turns;
-        int head;
-        const int kind = __builtin_amdgcn_readfirstlane(kind_at(a, (int)(item - row * a.turns), 1, &head));
-        const Heads& h = a.of[kind];
-        const E* from = static_cast<const E*>(h.x) + row * h.stride + (int64_t)head * a.dim;
-        // pairs lane and lane + 64, singles lane, lane + 64, ... : at most 256 elements
-        float p[2][2] = {}, single[4] = {};
-        int at[2][2] = {};
-        float sum = 0.0f;
+    // elements of this lane: pairs lane and lane + 64, singles lane, lane + 64, ... : 256 in all
+    int at[2][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = lane + 64 * i;
-            at[i][0] = a.interleaved ? 2 * n : n;
-            at[i][1] = a.interleaved ? 2 * n + 1 : n + half;
-            if (n < half)
+    for (int i = 0; i < 2; ++i) {
+        const int n = lane + 64 * i;
+        at[i][0] = a.interleaved ? 2 * n : n;
+        at[i][1] = a.interleaved ? 2 * n + 1 : n + half;
+    }
+    struct Head {
+        E pair[2][2], single[4];
+    };
+    for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items; item += (int64_t)gridDim.x * kWaves) {
+        const int64_t row = spans == 1 ? item : item / spans;
+        const int begin = (int)(item - row * spans) * a.span, end = begin + a.span < a.turns ? begin + a.span : a.turns;
+        auto load = [&](int turn, Head& x) {
+            int head;
+            const int kind = __builtin_amdgcn_readfirstlane(kind_at(a, turn, 1, &head));
+            const Heads& h = a.of[kind];
+            const E* from = static_cast<const E*>(h.x) + row * h.stride + (int64_t)head * a.dim;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    p[i][e] = (float)from[at[i][e]];
-                    sum += p[i][e] * p[i][e];
+                    x.pair[i][e] = E(0);
+                    if (lane + 64 * i < half)
+                        x.pair[i][e] = from[at[i][e]];
                 }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 64 * i < singles) {
-                single[i] = (float)from[a.rotated + lane + 64 * i];
-                sum += single[i] * single[i];
+            for (int i = 0; i < 4; ++i) {
+                x.single[i] = E(0);
+                if (lane + 64 * i < singles)
+                    x.single[i] = from[a.rotated + lane + 64 * i];
             }
-        float by = 1.0f;
-        const bool normed = kind != kValue && a.norm;
-        if (normed) {
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1)
-                sum += __shfl_xor(sum, d);
-            by = __builtin_amdgcn_rsqf(sum / (float)a.dim + a.eps);
-        }
-        auto scaled = [&](float x, int d) {
-            return !normed ? x : h.weight != nullptr ? x * by * weight_at(h.weight, a.weight_dtype, d) : x * by;
         };
-        int64_t head_stride;
-        O* to = row_out<OUT>(a, kind, row, &head_stride);
-        if (to == nullptr)
-            continue;
-        to += head * head_stride;
+        Head next;
+        load(begin, next);
+        const int position = a.positions[row];
+        float2 t[2] = {};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = lane + 64 * i;
-            if (n >= half)
-                continue;
-            float x = scaled(p[i][0], at[i][0]), y = scaled(p[i][1], at[i][1]);
-            if (kind != kValue) {
-                const float2 t = turn_of(a.positions[row], a.freqs[n]);
-                const float u = x * t.x - y * t.y;
-                y = y * t.x + x * t.y;
-                x = u;
+        for (int i = 0; i < 2; ++i)
+            if (lane + 64 * i < half)
+                t[i] = turn_of(position, a.freqs[lane + 64 * i]);
+        for (int turn = begin; turn < end; ++turn) {
+            int head;
+            const int kind = __builtin_amdgcn_readfirstlane(kind_at(a, turn, 1, &head));
+            const Heads& h = a.of[kind];
+            const Head x = next;
+            if (turn + 1 < end)
+                load(turn + 1, next);
+            const bool normed = kind != kValue && a.norm;
+            float by = 1.0f;
+            if (normed) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    sum += (float)x.pair[i][0] * (float)x.pair[i][0] + (float)x.pair[i][1] * (float)x.pair[i][1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum += (float)x.single[i] * (float)x.single[i];
+                sum = wave_sum(sum);
+                by = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, a.per_element, a.eps));
             }
-            to[at[i][0]] = (O)x;
-            to[at[i][1]] = (O)y;
-        }
+            auto scaled = [&](E e, int d) {
+                const float v = (float)e;
+                return !normed ? v : h.weight != nullptr ? v * by * weight_at(h.weight, a.weight_dtype, d) : v * by;
+            };
+            int64_t head_stride;
+            O* to = row_out<OUT>(a, kind, row, &head_stride);
+            if (to == nullptr)
+                continue;
+            to += head * head_stride;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 64 * i < singles)
-                to[a.rotated + lane + 64 * i] = (O)scaled(single[i], a.rotated + lane + 64 * i);
+            for (int i = 0; i < 2; ++i) {
+                if (lane + 64 * i >= half)
+                    continue;
+                float p = scaled(x.pair[i][0], at[i][0]), q = scaled(x.pair[i][1], at[i][1]);
+                if (kind != kValue) {
+                    const float u = p * t[i].x - q * t[i].y;
+                    q = q * t[i].x + p * t[i].y;
+                    p = u;
+                }
+                to[at[i][0]] = (O)p;
+                to[at[i][1]] = (O)q;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (lane + 64 * i < singles)
+                    to[a.rotated + lane + 64 * i] = (O)scaled(x.single[i], a.rotated + lane + 64 * i);
+        }
     }
 }
 
