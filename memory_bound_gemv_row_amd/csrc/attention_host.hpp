@@ -106,7 +106,8 @@ inline int chunk_for(int64_t items, int limit, int dim, int cus)
     return best;
 }
 
-inline Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q_heads, bool weighted, int cus)
+inline Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int q_heads, bool weighted, int cus,
+                       bool may_be_lone = true)
 {
     Split p;
     const int group = q_heads / c->heads;
@@ -118,7 +119,7 @@ inline Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit
     // key-value heads of 256 slots 7.5 us against 9.5, of 512 slots 11.3 against
     // 8.8; 128 of them, which fill half the card, 512 slots 12.3 against 17.6, 768
     // 15.8 against 16.7.
-    p.lone = whole_tiles(c) && chunk < limit && (limit <= 256 || (limit <= 768 && items * 2 >= cus));
+    p.lone = may_be_lone && whole_tiles(c) && chunk < limit && (limit <= 256 || (limit <= 768 && items * 2 >= cus));
     if (p.lone)
         chunk = (limit + 63) / 64 * 64;
     p.chunk = chunk;

@@ -80,17 +80,24 @@ constexpr float kSlack = 8.0f;   // powers of two that a logit may pass the refe
 // in whole tiles, are cut out of the length (slot j past the first tokens'
 // tiles is slot j + gap of the sequence), so only the window's first tile and the
 // first tokens' last hold slots that are not seen; these are not read.
-template <int DT, int DP, bool WHOLE, bool EXACT, int WAVES, bool VIEW = false>
-__global__ void __launch_bounds__(WAVES * 64, DP == 256 ? 1 : 2)
-attention_kernel(Attention a)
+template <int DP, bool WHOLE, int WAVES>
+struct AttentionShared {
+    float red_m[WAVES][16];
+    float red_s[WAVES][16];
+    __attribute__((aligned(16))) float red_o[WAVES][16][DP];
+    int32_t slot_page[WHOLE ? 1 : kMaxChunk];
+};
+
+template <int DT, int DP, bool WHOLE, bool EXACT, int WAVES, bool VIEW>
+__device__ __forceinline__ void attention_block(const Attention& a, int block, AttentionShared<DP, WHOLE, WAVES>& shared)
 {
     constexpr int kSteps = DP / 32;              // of 32 elements of the dot products
     constexpr int VW = DP == 64 ? 4 : 8;         // elements of a value row per lane and set
     constexpr int kSets = DP / (16 * VW);
     constexpr int kWords = VW / 2;
-    __shared__ float red_m[WAVES][16];
-    __shared__ float red_s[WAVES][16];
-    __shared__ __attribute__((aligned(16))) float red_o[WAVES][16][DP];
+    auto& red_m = shared.red_m;
+    auto& red_s = shared.red_s;
+    auto& red_o = shared.red_o;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -103,8 +110,8 @@ attention_kernel(Attention a)
     // spread over all XCDs.
     // Where a head's queries need several workgroups, those that read the same
     // keys are a multiple of eight apart: on one XCD, at about the same time.
-    const int turn = (int)blockIdx.x / a.heads;
-    const int kv = ((int)blockIdx.x + turn) % a.heads;
+    const int turn = block / a.heads;
+    const int kv = (block + turn) % a.heads;
     int tile = 0, range = turn;
     if (a.tiles > 1) {
         const int eight = turn / (8 * a.tiles), rest = turn - eight * 8 * a.tiles;
@@ -177,7 +184,7 @@ attention_kernel(Attention a)
     // the pages of this part, looked up once so that no tile's loads wait for
     // a page number: WHOLE, tile t of this wave in lane t; otherwise every slot's in LDS
     int pages = -1;
-    __shared__ int32_t slot_page[WHOLE ? 1 : kMaxChunk];
+    auto& slot_page = shared.slot_page;
     if constexpr (WHOLE) {
         const int64_t j = (int64_t)begin + (wave + lane * WAVES) * 16;
         if (VIEW ? j < end : j < a.at.limit)
@@ -380,6 +387,14 @@ attention_kernel(Attention a)
                 narrow_to<DT>(a.out, row * a.dim + d + k, total == 0.0f ? 0.0f : o[k] / total);
         }
     }
+}
+
+template <int DT, int DP, bool WHOLE, bool EXACT, int WAVES, bool VIEW = false>
+__global__ void __launch_bounds__(WAVES * 64, DP == 256 ? 1 : 2)
+attention_kernel(Attention a)
+{
+    __shared__ AttentionShared<DP, WHOLE, WAVES> shared;
+    attention_block<DT, DP, WHOLE, EXACT, WAVES, VIEW>(a, blockIdx.x, shared);
 }
 
 // The maximum and the sum of powers of a query head over the parts that its

@@ -22,16 +22,22 @@ struct Tiling {
     size_t ms_at, out_at, bytes;
 };
 
-// The least estimate, in steps of a tile of keys: what the busiest of the places
-// for workgroups does (two per CU, one for heads over 128).  All the work spread
-// over the places, with `kStart` for a workgroup's start and end, and half of
-// the longest workgroup for an uneven end; or, where there is a place for each,
-// the longest one.  A join costs a launch, and the parts written and read: a step
-// takes about 2.3 us for heads of 128, in which memory moves 10 MB.
+// The least estimate, in us.  A workgroup takes a step for each tile of keys and
+// kStart for its start and end; a step takes 2.15 us for heads of 128 where a CU
+// holds two workgroups (one for heads over 128), less where it holds one.  As
+// many as there are places for start together, and where they see alike the next
+// ones wait for them: a round that is half empty costs as much as a full one
+// (4 x 7 tokens over 65543 keys: 16 parts, one round, 148 us; 20 parts 170, 32
+// parts 155).  Where a sequence's newest tokens are most of it they see fewer keys
+// the earlier they are, and the work spreads evenly but for its end.  A join
+// costs a launch, its parts written and read at 6 TB/s, kPart for each of a row's,
+// and its waves: 8192 at a time for 3.5 us (7943 rows of 16 heads in two parts: 155
+// us, 91 without).  `per_cu`: workgroups that a CU holds (two, for heads up to
+// 128, three up to 64), or that it takes of these beside others.
 Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int limit, int window, int sinks, int max_new,
-                 int cus)
+                 double per_cu, int cus)
 {
-    constexpr double kStart = 3, kJoin = 2;
+    constexpr double kStart = 1.5, kJoin = 4.0, kMoved = 6e6, kPart = 0.06, kWave = 3.5 / 8192;
     Tiling t{};
     t.tiles = rows * group / kTileRows + batch;
     int64_t keys = ((int64_t)limit + kTileKeys - 1) / kTileKeys;
@@ -41,20 +47,23 @@ Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int
         keys = seen < keys ? seen : keys;
     }
     keys = keys > 0 ? keys : 1;
-    // of a sequence whose newest tokens are many, the first of them see fewer keys
-    const int64_t late = (int64_t)limit - max_new / 2;
-    const double mean = (double)keys < (double)late / kTileKeys + 1 ? (double)keys : (double)late / kTileKeys + 1;
+    const bool uneven = max_new > limit / 2 && window == 0;
+    const double mean = uneven ? (double)(limit - max_new / 2) / kTileKeys + 1 : (double)keys;
     const int64_t each = (rows + batch - 1) / (batch > 0 ? batch : 1);   // new tokens of a sequence, about
     const double items = (double)c->heads * batch * (double)((each * group + kTileRows - 1) / kTileRows);
-    const double places = cus * (c->head_dim > 128 ? 1.0 : 2.0);
-    const double moved = (double)rows * group * c->heads * 8 * 128 / 10e6;   // in steps, for each part
+    const double places = cus * per_cu * (c->head_dim > 128 ? 0.5 : waves_of(c->head_dim) / 2.0);
+    const double step = 2.15 * (c->head_dim > 64 ? c->head_dim : 64) / 128;
+    const double heads = (double)rows * group * c->heads, moved = heads * c->head_dim * 8;   // bytes of each part
     double least = 0;
     for (int64_t parts = 1; parts <= keys && parts <= 256; ++parts) {
         const int64_t chunk = (keys + parts - 1) / parts;
         if ((keys + chunk - 1) / chunk != parts)
             continue;
-        const double all = items * (mean + kStart * parts) / places, longest = chunk + kStart;
-        const double cost = (items * parts <= places ? longest : all + longest / 2) + (parts > 1 ? kJoin + moved * parts : 0);
+        const double longest = chunk + kStart, rounds = items * parts / places;
+        double steps = rounds <= 1 ? longest : uneven ? items * (mean + kStart * parts) / places + longest / 2 : ceil(rounds) * longest;
+        if (items * parts <= cus)
+            steps *= 0.75;
+        const double cost = steps * step + (parts > 1 ? kJoin + moved * parts / kMoved + kPart * parts + heads * kWave : 0);
         if (t.parts == 0 || cost < least) {
             least = cost;
             t.parts = (int)parts;
@@ -115,30 +124,46 @@ const void* view_for(const gemv_kv_cache* c, bool lone)
                             : view_sized<DT, false, kWaves>(c->head_dim);
 }
 
-template <int DT, bool WHOLE>
-const void* prompt_sized(int dim)
+enum Form { kPrompt, kPrefix };
+
+template <int DT, int DP, int RUN, bool EXACT>
+const void* form_of(Form form)
 {
-    if constexpr (WHOLE) {
-        if (dim == 64)
-            return reinterpret_cast<const void*>(&prompt_kernel<DT, 64, true, true>);
-        if (dim == 96)
-            return reinterpret_cast<const void*>(&prompt_kernel<DT, 96, true, true>);
-        if (dim == 128)
-            return reinterpret_cast<const void*>(&prompt_kernel<DT, 128, true, true>);
-        if (dim == 256)
-            return reinterpret_cast<const void*>(&prompt_kernel<DT, 256, true, true>);
-    }
-    return dim <= 64    ? reinterpret_cast<const void*>(&prompt_kernel<DT, 64, WHOLE, false>)
-           : dim <= 96  ? reinterpret_cast<const void*>(&prompt_kernel<DT, 96, WHOLE, false>)
-           : dim <= 128 ? reinterpret_cast<const void*>(&prompt_kernel<DT, 128, WHOLE, false>)
-                        : reinterpret_cast<const void*>(&prompt_kernel<DT, 256, WHOLE, false>);
+    return form == kPrompt ? reinterpret_cast<const void*>(&prompt_kernel<DT, DP, RUN, EXACT>)
+                           : reinterpret_cast<const void*>(&prefix_kernel<DT, DP, RUN, EXACT>);
 }
 
-const void* prompt_for(const gemv_kv_cache* c)
+template <int DT, int RUN>
+const void* tiled_sized(Form form, int dim)
 {
-    if (c->dtype == GEMV_F16)
-        return whole_tiles(c) ? prompt_sized<kF16, true>(c->head_dim) : prompt_sized<kF16, false>(c->head_dim);
-    return whole_tiles(c) ? prompt_sized<kBF16, true>(c->head_dim) : prompt_sized<kBF16, false>(c->head_dim);
+    if constexpr (RUN == 16) {
+        if (dim == 64)
+            return form_of<DT, 64, 16, true>(form);
+        if (dim == 96)
+            return form_of<DT, 96, 16, true>(form);
+        if (dim == 128)
+            return form_of<DT, 128, 16, true>(form);
+        if (dim == 256)
+            return form_of<DT, 256, 16, true>(form);
+    }
+    if (dim > 64 && dim <= 96)   // rows of 12 pieces: a load's are not of one run of 8
+        return form_of<DT, 96, RUN == 8 ? 1 : RUN, false>(form);
+    return dim <= 64    ? form_of<DT, 64, RUN, false>(form)
+           : dim <= 128 ? form_of<DT, 128, RUN, false>(form) : form_of<DT, 256, RUN, false>(form);
+}
+
+template <int DT>
+const void* tiled_typed(Form form, const gemv_kv_cache* c)
+{
+    if (whole_tiles(c))
+        return tiled_sized<DT, 16>(form, c->head_dim);
+    return c->page_size % 8 == 0 && c->stride_slot < (1 << 26) ? tiled_sized<DT, 8>(form, c->head_dim)
+                                                               : tiled_sized<DT, 1>(form, c->head_dim);
+}
+
+const void* tiled_for(Form form, const gemv_kv_cache* c)
+{
+    return c->dtype == GEMV_F16 ? tiled_typed<kF16>(form, c) : tiled_typed<kBF16>(form, c);
 }
 
 // Few rows are joined by four waves each, where there are parts enough for them.
@@ -246,7 +271,7 @@ Plan plan_prompt(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int 
         return p;
     }
     p.tiling = tile_rows(c, rows, s->batch, q_heads / c->heads, limit, p.window, p.sinks,
-                         max_new < rows ? max_new : rows, cus);
+                         max_new < rows ? max_new : rows, 2.0, cus);
     p.joined = p.tiling.parts > 1;
     place_parts(&p.tiling, 0, heads, c->head_dim, p.joined);
     p.bytes = p.tiling.bytes;
@@ -264,11 +289,13 @@ PrefixPlan plan_prefix(const gemv_kv_cache* c, const gemv_kv_batch* prefixes, co
 {
     PrefixPlan p{};
     const int64_t heads = (int64_t)s->batch * q_heads;
-    p.shared = tile_rows(c, s->batch, prefixes->batch, q_heads / c->heads, far_limit, 0, 0, 0, cus);
+    // one place and a half: the others are for the sequences' own tokens (128 sequences
+    // behind two prefixes of up to 32768: 118 us with 12 parts, 127 with 16, 140 with 8)
+    p.shared = tile_rows(c, s->batch, prefixes->batch, q_heads / c->heads, far_limit, 0, 0, 0, 1.5, cus);
     if (prefixes->batch == 0 || far_limit == 0)
         p.shared.parts = 0;
     place_parts(&p.shared, 0, heads, c->head_dim, true);
-    p.own = split_for(c, s, limit, q_heads, false, cus);
+    p.own = split_for(c, s, limit, q_heads, false, cus, false);
     if (limit == 0)
         p.own.parts = 0;
     p.own_ms_at = p.shared.bytes;
@@ -363,7 +390,8 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
         return join_parts(j, cache->dtype, dev.cus, stream);
     }
     const int64_t grid = p.tiling.tiles * cache->heads * p.tiling.parts;
-    if (!fits(grid, 256))
+    const int block = 256 * outputs_of(cache->head_dim);
+    if (!fits(grid, block))
         return GEMV_E_UNSUPPORTED;
     Prompt a = tiled(cache, at, batch->batch, starts, rows, p.tiling, q, q_stride, q_heads, scale, ws, p.joined);
     a.causal = true;
@@ -373,7 +401,7 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
     a.sink_tiles = whole_sinks(p.sinks, kTileKeys, at.limit) / kTileKeys;
     a.out = out;
     void* args[] = {(void*)&a};
-    if (int rc = launch(prompt_for(cache), grid, 256, args, stream); rc != GEMV_OK || !p.joined)
+    if (int rc = launch(tiled_for(kPrompt, cache), grid, block, args, stream); rc != GEMV_OK || !p.joined)
         return rc;
     j.from[0] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
     return join_parts(j, cache->dtype, dev.cus, stream);
@@ -417,10 +445,10 @@ int gemv_prefix_attention(const gemv_kv_cache* cache, const gemv_kv_batch* prefi
     const PrefixPlan p = plan_prefix(cache, prefixes, batch, far.limit, at.limit, q_heads, dev.cus);
     if (!holds(workspace, workspace_bytes, p.bytes))
         return GEMV_E_INVAL;
-    const int64_t far_grid = p.shared.tiles * cache->heads * p.shared.parts;
-    const int64_t grid = p.own.parts > 0 ? newest_grid(cache, batch->batch, p.own) : 0;
-    const int block = (p.own.lone ? kLoneWaves : kWaves) * 64;
-    if (!fits(far_grid, 256) || !fits(grid, block) || !joins_fit(batch->batch, q_heads))
+    const int64_t far_count = p.shared.tiles * cache->heads * p.shared.parts, far_blocks = (far_count + 7) / 8 * 8;
+    const int64_t near_count = p.own.parts > 0 ? newest_grid(cache, batch->batch, p.own) : 0;
+    const int block = 256 * outputs_of(cache->head_dim);
+    if (!fits(far_blocks + near_count, block) || !joins_fit(batch->batch, q_heads))
         return GEMV_E_UNSUPPORTED;
     char* ws = static_cast<char*>(workspace);
     Join j{};
@@ -428,21 +456,18 @@ int gemv_prefix_attention(const gemv_kv_cache* cache, const gemv_kv_batch* prefi
     j.q_heads = q_heads;
     j.dim = cache->head_dim;
     j.out = out;
-    if (far_grid > 0) {
-        Prompt a = tiled(cache, far, prefixes->batch, starts, batch->batch, p.shared, q, q_stride, q_heads, scale, ws, true);
-        void* args[] = {(void*)&a};
-        if (int rc = launch(prompt_for(cache), far_grid, 256, args, stream); rc != GEMV_OK)
+    Prompt f = tiled(cache, far, prefixes->batch, starts, batch->batch, p.shared, q, q_stride, q_heads, scale, ws, true);
+    Attention n = newest(cache, at, batch->batch, p.own, q, q_stride, q_heads, scale, ws, p.own_ms_at, p.own_out_at, true);
+    n.rows = batch->batch;
+    if (far_count > 0)
+        j.from[0] = Source{f.part_ms, f.part_out, f.parts, starts, prefixes->batch};
+    if (near_count > 0)
+        j.from[1] = Source{n.part_ms, n.part_out, n.parts, nullptr, 0};
+    if (far_blocks + near_count > 0) {
+        int blocks = (int)far_blocks, count = (int)far_count;
+        void* args[] = {(void*)&f, (void*)&n, (void*)&blocks, (void*)&count};
+        if (int rc = launch(tiled_for(kPrefix, cache), far_blocks + near_count, block, args, stream); rc != GEMV_OK)
             return rc;
-        j.from[0] = Source{a.part_ms, a.part_out, a.parts, starts, prefixes->batch};
-    }
-    if (grid > 0) {
-        Attention a = newest(cache, at, batch->batch, p.own, q, q_stride, q_heads, scale, ws, p.own_ms_at, p.own_out_at, true);
-        a.rows = batch->batch;
-        void* args[] = {(void*)&a};
-        const void* fn = cache->dtype == GEMV_F16 ? view_for<kF16>(cache, p.own.lone) : view_for<kBF16>(cache, p.own.lone);
-        if (int rc = launch(fn, grid, block, args, stream); rc != GEMV_OK)
-            return rc;
-        j.from[1] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
     }
     return join_parts(j, cache->dtype, dev.cus, stream);
 }

@@ -9,7 +9,7 @@
 // two products, few rows by memory.
 #pragma once
 
-#include "paged.hpp"
+#include "attention_kernels.hpp"
 
 namespace gattn {
 
@@ -22,6 +22,15 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr int kTileRows = 128;   // query rows of a workgroup, 32 a wave
 constexpr int kTileKeys = 64;    // keys of a step, 16 loaded by each wave
 constexpr int kEverySlot = 0x7FFFFFFE;
+
+// Waves that have the same 32 rows, and share out the output's elements: heads of
+// over 128 need two, for the sums of 256 elements leave no registers to work with.
+constexpr int outputs_of(int dim) { return dim > 128 ? 2 : 1; }
+
+// Waves of a SIMD that registers are shared out for.  Heads of 64 have as many
+// exponentials for half the matrix products and gain by a third wave (6 x 1999
+// tokens of 16 heads: 79.9 -> 69.1 us; a fourth leaves too few registers, 83.2).
+constexpr int waves_of(int dim) { return dim > 64 ? 2 : 3; }
 
 struct Prompt {
     Pages at;
@@ -176,9 +185,10 @@ __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 
 // One workgroup: 128 query rows (tokens times the query heads of one key-value
 // head, a token's heads together) of one sequence, over one part of the keys
-// that any of them sees.  Each wave has 32 rows; the four load 64 keys and
-// values at a time straight to LDS, into one of two buffers while the other is
-// multiplied.
+// that any of them sees.  Each wave has 32 rows (heads of over 128: two waves
+// have the same, take the same logits, and half of the output each); they load
+// 64 keys and values at a time straight to LDS, into one of two buffers while the
+// other is multiplied.
 //
 // Logits: v_mfma_f32_32x32x16 with keys as rows and queries, which stay in
 // registers, as columns: lane l gets, for query row l % 32, the logits of keys
@@ -192,6 +202,11 @@ __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 // 2^-8 relative each, is below that of the output, which averages over them;
 // the sum is taken over the rounded powers, so the weights still add up to one.
 //
+// RUN: slots that lie in one page from their first multiple on, 16 or 8, whose
+// address is the same for all lanes; 1: each row has an address of its own (4 x
+// 8192 tokens, 16 heads of 64: 586 us in pages of 16, 617 in pages of 24, 682 with
+// an address for each row).
+//
 // Places in LDS: piece c (16 bytes) of key row r lies at c ^ swizzle(r), such
 // that the 16 rows that a read of keys takes at a time, and the four rows of
 // 64 bytes that a read of values does, are in different banks.
@@ -200,19 +215,26 @@ __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 // There the values may hold NaN or infinities in slots that only some rows
 // see; 0 * NaN would bring them to the others, so where there are any such a tile
 // is multiplied key by key, and rows that do not see the key keep their sums.
-template <int DT, int DP, bool WHOLE, bool EXACT>
-__global__ void __launch_bounds__(256, DP == 256 ? 1 : 2)
-prompt_kernel(Prompt a)
+template <int DP>
+struct PromptShared {
+    u32x4 buffers[2][2][kTileKeys * DP / 8];                    // keys and values of a step, and of the next
+    __attribute__((aligned(8))) uint16_t held_bits[2][4];       // bit per key: its slot is there
+};
+
+template <int DT, int DP, int RUN, bool EXACT>
+__device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptShared<DP>& shared)
 {
     constexpr int CH = DP / 8;        // pieces of a row
     constexpr int kLoads = CH / 4;    // 64 pieces each of the 16 rows that a wave loads
     constexpr int kSteps = DP / 16;   // of 16 elements of the dot products
-    constexpr int kBlocks = DP / 32;  // of 32 elements of the output
-    __shared__ u32x4 buffers[2][2][kTileKeys * CH];                    // keys and values of a step, and of the next
-    __shared__ __attribute__((aligned(8))) uint16_t held_bits[2][4];   // bit per key: its slot is there
+    constexpr int kOutputs = outputs_of(DP);
+    constexpr int kBlocks = DP / 32 / kOutputs;   // of 32 elements of the output
+    auto& buffers = shared.buffers;
+    auto& held_bits = shared.held_bits;
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6 & 3);
+    const int output = kOutputs == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int half = lane >> 5;
 
     // Workgroups go to the eight XCDs in turn.  Those that read the same keys
@@ -226,12 +248,12 @@ prompt_kernel(Prompt a)
     auto quotient = [&](int x, int y) { return one((int)((unsigned)x / (unsigned)y)); };
     int set, place;
     if (sets % 8 == 0) {
-        const int j = (int)blockIdx.x >> 3, m = quotient(j, a.tiles);
-        set = m * 8 + ((int)blockIdx.x & 7);
+        const int j = block >> 3, m = quotient(j, a.tiles);
+        set = m * 8 + (block & 7);
         place = j - m * a.tiles;
     } else {
-        place = quotient((int)blockIdx.x, sets);
-        set = (int)blockIdx.x - place * sets;
+        place = quotient(block, sets);
+        set = block - place * sets;
     }
     const int part_back = quotient(set, a.heads), part = a.parts - 1 - part_back;
     const int kv_at = set - part_back * a.heads + part;
@@ -296,30 +318,43 @@ prompt_kernel(Prompt a)
     auto value_swizzle = [](int row) {
         return DP == 64 ? (row >> 1 & 1) << 2 : DP == 96 ? 0 : (row & 3) << 2;
     };
-    const uint16_t* k0 = a.k + kv * a.at.stride_head;
-    const uint16_t* v0 = a.v + kv * a.at.stride_head;
+    // of keys and of values, or where two waves have the same rows, of one of them
+    constexpr int kKinds = 2 / kOutputs;
+    const uint16_t* pool[kKinds];
     int load_row[kLoads];
-    unsigned key_piece[kLoads], value_piece[kLoads];   // bytes from the row's start; WHOLE: from the 16 rows' start
+    unsigned piece[kKinds][kLoads];   // bytes from the row's start; of runs: from the run's first row's
+    constexpr bool kRun = RUN > 1;
+    constexpr int kRuns = kRun ? 16 / RUN : 1;
+    static_assert(RUN != 8 || 8 * CH % 64 == 0, "a load has rows of one run");
+    auto run_of = [](int i) { return kRun ? i * 64 / CH / RUN : 0; };   // of load i
+#pragma unroll
+    for (int x = 0; x < kKinds; ++x)
+        pool[x] = (x + output == 0 ? a.k : a.v) + kv * a.at.stride_head;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int p = i * 64 + lane, rw = p / CH, c = p - rw * CH;
-        const int kc = c ^ key_swizzle(rw), vc = c ^ value_swizzle(rw);
-        const unsigned first = WHOLE ? (unsigned)(rw * (int)a.at.stride_slot) * 2 : 0u;
-        load_row[i] = rw;
-        key_piece[i] = EXACT || kc * 8 < a.dim ? first + kc * 16 : kNowhere;
-        value_piece[i] = EXACT || vc * 8 < a.dim ? first + vc * 16 : kNowhere;
+        load_row[i] = rw - run_of(i) * RUN;
+#pragma unroll
+        for (int x = 0; x < kKinds; ++x) {
+            const int at = c ^ (x + output == 0 ? key_swizzle(rw) : value_swizzle(rw));
+            const unsigned first = kRun ? (unsigned)(load_row[i] * (int)a.at.stride_slot) * 2 : 0u;
+            piece[x][i] = EXACT || at * 8 < a.dim ? first + at * 16 : kNowhere;
+        }
     }
     struct Place {
-        int page[WHOLE ? 1 : kLoads];
+        int page[kRun ? kRuns : kLoads];
     };
     // the pages of step u, looked up a step before its loads
     auto look = [&](int u) {
         Place w;
         const int j = slot_of(u) + 16 * wave;
-        if constexpr (WHOLE) {
-            w.page[0] = -1;
-            if (u < end && j < len)
-                w.page[0] = shared_word(a.at.table + b * a.at.table_stride + a.at.page_of.by(j));
+        if constexpr (kRun) {
+#pragma unroll
+            for (int g = 0; g < kRuns; ++g) {
+                w.page[g] = -1;
+                if (u < end && j + g * RUN < len)
+                    w.page[g] = shared_word(a.at.table + b * a.at.table_stride + a.at.page_of.by(j + g * RUN));
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
@@ -330,23 +365,32 @@ prompt_kernel(Prompt a)
         }
         return w;
     };
-    const unsigned wave_byte = __builtin_amdgcn_readfirstlane(lds_byte(&buffers[0][0][0])) + wave * 16 * CH * 16;
     constexpr unsigned kHalfBytes = kTileKeys * CH * 16;
+    const unsigned wave_byte = __builtin_amdgcn_readfirstlane(lds_byte(&buffers[0][output][0])) + wave * 16 * CH * 16;
     auto fetch = [&](int which, int u, const Place& w) {
         const int j = slot_of(u) + 16 * wave;
-        const unsigned place_k = wave_byte + which * 2 * kHalfBytes, place_v = place_k + kHalfBytes;
+        const unsigned to = wave_byte + which * 2 * kHalfBytes;
         unsigned bits;
-        if constexpr (WHOLE) {
-            const bool is = (unsigned)w.page[0] < (unsigned)a.at.pages;
-            const int left = is ? len - j : 0;
-            const int64_t at = is ? w.page[0] * a.at.stride_page + (int64_t)(j - a.at.page_of.by(j) * a.at.page_size) * a.at.stride_slot : 0;
-            const u32x4 keys = descriptor(k0 + at, is ? kNowhere - 1 : 0), values = descriptor(v0 + at, is ? kNowhere - 1 : 0);
+        if constexpr (kRun) {
+            bits = 0;
+            u32x4 from[kRuns][kKinds];
+            int left[kRuns];   // slots of the run before the end
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                piece_to_lds(keys, load_row[i] < left ? key_piece[i] : kNowhere, place_k + i * 1024);
-                piece_to_lds(values, load_row[i] < left ? value_piece[i] : kNowhere, place_v + i * 1024);
+            for (int g = 0; g < kRuns; ++g) {
+                const int jg = j + g * RUN;
+                const bool is = (unsigned)w.page[g] < (unsigned)a.at.pages;
+                left[g] = is ? len - jg : 0;
+                const int64_t at = is ? w.page[g] * a.at.stride_page + (int64_t)(jg - a.at.page_of.by(jg) * a.at.page_size) * a.at.stride_slot : 0;
+#pragma unroll
+                for (int x = 0; x < kKinds; ++x)
+                    from[g][x] = descriptor(pool[x] + at, is ? kNowhere - 1 : 0);
+                bits |= (left[g] >= RUN ? (1u << RUN) - 1u : (1u << (left[g] > 0 ? left[g] : 0)) - 1u) << (g * RUN);
             }
-            bits = left >= 16 ? 0xFFFFu : (1u << (left > 0 ? left : 0)) - 1u;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+                for (int x = 0; x < kKinds; ++x)
+                    piece_to_lds(from[run_of(i)][x], load_row[i] < left[run_of(i)] ? piece[x][i] : kNowhere, to + x * kHalfBytes + i * 1024);
         } else {
             bits = 0;
 #pragma unroll
@@ -354,10 +398,11 @@ prompt_kernel(Prompt a)
                 const int s = j + load_row[i];
                 const bool is = s < len && (unsigned)w.page[i] < (unsigned)a.at.pages;
                 const int64_t at = is ? w.page[i] * a.at.stride_page + (int64_t)(s - a.at.page_of.by(s) * a.at.page_size) * a.at.stride_slot : 0;
-                const char* const ks = reinterpret_cast<const char*>(k0 + at), * const vs = reinterpret_cast<const char*>(v0 + at);
-                const char* const zeros = reinterpret_cast<const char*>(kZeros);
-                piece_to_lds(is && key_piece[i] != kNowhere ? ks + key_piece[i] : zeros, place_k + i * 1024);
-                piece_to_lds(is && value_piece[i] != kNowhere ? vs + value_piece[i] : zeros, place_v + i * 1024);
+#pragma unroll
+                for (int x = 0; x < kKinds; ++x)
+                    piece_to_lds(is && piece[x][i] != kNowhere ? reinterpret_cast<const char*>(pool[x] + at) + piece[x][i]
+                                                               : reinterpret_cast<const char*>(kZeros),
+                                 to + x * kHalfBytes + i * 1024);
                 // a row's first piece speaks for it
                 const uint64_t lanes = __ballot(is);
 #pragma unroll
@@ -366,7 +411,7 @@ prompt_kernel(Prompt a)
                         bits |= (unsigned)(lanes >> (rw * CH - i * 64) & 1) << rw;
             }
         }
-        if (lane == 0)
+        if (lane == 0 && output == 0)
             held_bits[which][wave] = (uint16_t)bits;
     };
 
@@ -381,7 +426,7 @@ prompt_kernel(Prompt a)
     auto key_piece_at = [&](int t, int e) { return (32 * t + key_row) * CH + ((2 * e) ^ key_base); };
     // four and four keys of step `step` (16 keys), 32 columns from 32 `block` on
     auto value = [&](const u32x4* values, int step, int block) {
-        const unsigned byte = value_byte + (unsigned)((4 * block + value_col) ^ value_base) * 16;
+        const unsigned byte = value_byte + (unsigned)((4 * (kBlocks * output + block) + value_col) ^ value_base) * 16;
         const u32x2 x = column_of_four(values, byte + (unsigned)(16 * step) * CH * 16);
         const u32x2 y = column_of_four(values, byte + (unsigned)(16 * step + 8) * CH * 16);
         return u32x4{x.x, x.y, y.x, y.y};
@@ -572,7 +617,7 @@ prompt_kernel(Prompt a)
     const int64_t at = row * a.q_heads + head;
     if (a.part_out != nullptr) {
         const int64_t to_part = at * a.parts + part;
-        if (half == 0) {
+        if (half == 0 && output == 0) {
             a.part_ms[to_part * 2] = m == -kInf ? -kInf : m * a.scale;
             a.part_ms[to_part * 2 + 1] = sum;
         }
@@ -581,7 +626,7 @@ prompt_kernel(Prompt a)
             for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int d = 32 * k + 8 * i + 4 * half;
+                    const int d = 32 * (kBlocks * output + k) + 8 * i + 4 * half;
                     if (EXACT || d < a.dim)
                         *reinterpret_cast<f32x4*>(a.part_out + to_part * a.dim + d) =
                             f32x4{acc[k][4 * i], acc[k][4 * i + 1], acc[k][4 * i + 2], acc[k][4 * i + 3]};
@@ -594,7 +639,7 @@ prompt_kernel(Prompt a)
     for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int d = 32 * k + 8 * i + 4 * half;
+            const int d = 32 * (kBlocks * output + k) + 8 * i + 4 * half;
             u32x2 w = {0, 0};
             if (sum != 0.0f) {
                 w.x = narrow_pair<DT>(acc[k][4 * i] * by, acc[k][4 * i + 1] * by);
@@ -603,6 +648,34 @@ prompt_kernel(Prompt a)
             if (EXACT || d < a.dim)
                 *reinterpret_cast<u32x2*>(out + d) = w;
         }
+}
+
+template <int DT, int DP, int RUN, bool EXACT>
+__global__ void __launch_bounds__(256 * outputs_of(DP), waves_of(DP))
+prompt_kernel(Prompt a)
+{
+    __shared__ PromptShared<DP> shared;
+    prompt_block<DT, DP, RUN, EXACT>(a, blockIdx.x, shared);
+}
+
+// Shared prefixes and the sequences' own tokens in one launch: the first
+// `far_blocks` workgroups (a multiple of eight, so that the others too keep to
+// their XCDs) take the prefixes, which the matrix units bound, the others the
+// rest, which memory does; a CU that holds one of each is slowed by neither.
+template <int DT, int DP, int RUN, bool EXACT>
+__global__ void __launch_bounds__(256 * outputs_of(DP), waves_of(DP))
+prefix_kernel(Prompt far, Attention near, int far_blocks, int far_count)
+{
+    constexpr int NP = DP == 96 ? 128 : DP, kNearWaves = 4 * outputs_of(DP);
+    __shared__ union {
+        PromptShared<DP> far;
+        AttentionShared<NP, RUN == 16, kNearWaves> near;
+    } shared;
+    const int block = blockIdx.x;
+    if (block >= far_blocks)
+        attention_block<DT, NP, RUN == 16, RUN == 16 && EXACT && DP == NP, kNearWaves, true>(near, block - far_blocks, shared.near);
+    else if (block < far_count)
+        prompt_block<DT, DP, RUN, EXACT>(far, block, shared.far);
 }
 
 // Parts of the same rows: of `parts` each, in the layout of part_out and
