@@ -49,8 +49,8 @@ extern "C" {
  * GEMV_E_INVAL for negative sizes, a missing pointer (starts too, where max_new
  * is not 1 or rows < batch), window < 0 or sinks < 0, or too small a workspace;
  * GEMV_E_UNSUPPORTED as for gemv_attention, for out not 16-byte aligned,
- * and where a launch would pass 2^30 work-items (about 4 million tiles of 128
- * query rows, or joins of 4). */
+ * for more than 2^30 rows of heads, and where a launch would pass 2^30 work-items
+ * (about 4 million tiles of 128 query rows, or joins of 4). */
 size_t gemv_prompt_attention_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* batch, int rows, int max_new,
                                        int q_heads, int window, int sinks);
 

@@ -304,12 +304,18 @@ PrefixPlan plan_prefix(const gemv_kv_cache* c, const gemv_kv_batch* prefixes, co
     return p;
 }
 
-int check_query(const gemv_kv_cache* c, const void* q, int64_t q_stride, const void* out)
+int check_query(const void* q, int64_t q_stride, const void* out)
 {
     if (q == nullptr || out == nullptr)
         return GEMV_E_INVAL;
-    (void)c;
     return q_stride % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) ? GEMV_E_UNSUPPORTED : GEMV_OK;
+}
+
+// Rows, and sequences of heads, that no launch has work-items for, whose products
+// with what follows could pass 64 bits.
+bool countable(int64_t rows, int64_t q_heads, int64_t batch, int64_t heads)
+{
+    return rows * q_heads <= gemv_device::kMaxWorkItems && batch * heads <= gemv_device::kMaxWorkItems;
 }
 
 bool holds(const void* workspace, size_t bytes, size_t need)
@@ -328,7 +334,7 @@ size_t gemv_prompt_attention_workspace(const gemv_kv_cache* cache, const gemv_kv
     using namespace gattn;
     Pages at{};
     if (check(cache, batch, &at) != GEMV_OK || q_heads < 1 || q_heads % cache->heads != 0 || rows < 1 || max_new < 1 ||
-        window < 0 || sinks < 0 || batch->batch == 0)
+        window < 0 || sinks < 0 || batch->batch == 0 || !countable(rows, q_heads, batch->batch, cache->heads))
         return 0;
     gemv_device::Device dev{};
     if (gemv_device::current(&dev) != GEMV_OK)
@@ -351,8 +357,10 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
         return GEMV_E_INVAL;
     if (batch->batch == 0 || rows == 0 || max_new == 0)
         return GEMV_OK;
-    if (int rc = check_query(cache, q, q_stride, out); rc != GEMV_OK)
+    if (int rc = check_query(q, q_stride, out); rc != GEMV_OK)
         return rc;
+    if (!countable(rows, q_heads, batch->batch, cache->heads))
+        return GEMV_E_UNSUPPORTED;
     gemv_device::Device dev{};
     if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
         return rc;
@@ -413,7 +421,8 @@ size_t gemv_prefix_attention_workspace(const gemv_kv_cache* cache, const gemv_kv
     using namespace gattn;
     Pages at{}, far{};
     if (check(cache, batch, &at) != GEMV_OK || check(cache, prefixes, &far) != GEMV_OK || q_heads < 1 ||
-        q_heads % cache->heads != 0 || batch->batch == 0)
+        q_heads % cache->heads != 0 || batch->batch == 0 ||
+        !countable(batch->batch, q_heads, (int64_t)batch->batch + prefixes->batch, cache->heads))
         return 0;
     gemv_device::Device dev{};
     if (gemv_device::current(&dev) != GEMV_OK)
@@ -437,8 +446,10 @@ int gemv_prefix_attention(const gemv_kv_cache* cache, const gemv_kv_batch* prefi
         return GEMV_E_INVAL;
     if (batch->batch == 0)
         return GEMV_OK;
-    if (int rc = check_query(cache, q, q_stride, out); rc != GEMV_OK)
+    if (int rc = check_query(q, q_stride, out); rc != GEMV_OK)
         return rc;
+    if (!countable(batch->batch, q_heads, (int64_t)batch->batch + prefixes->batch, cache->heads))
+        return GEMV_E_UNSUPPORTED;
     gemv_device::Device dev{};
     if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
         return rc;

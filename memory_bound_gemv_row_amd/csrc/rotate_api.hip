@@ -30,6 +30,13 @@ int check_heads(const gemv_heads* h, int dim, int rows, bool own_out)
     return GEMV_OK;
 }
 
+// In place, or not at all: results laid over their inputs in another way would
+// meet elements that are still to be read.
+bool laid_alike(const gemv_heads* h, int in, int out)
+{
+    return h->out != h->x || h->out == nullptr || (in == out && h->stride == h->out_stride);
+}
+
 // 16 bytes of every row, head and piece
 bool wide(const gemv_heads* h, bool own_out)
 {
@@ -136,6 +143,8 @@ int gemv_norm_rotate(const gemv_rotation* how, const gemv_heads* q, const gemv_h
     }
     if (rows == 0)
         return GEMV_OK;
+    if (!laid_alike(q, dtype, out_dtype) || (k != nullptr && !laid_alike(k, dtype, out_dtype)))
+        return GEMV_E_INVAL;
     if (positions == nullptr || (how->rotated > 0 && how->freqs == nullptr))
         return GEMV_E_INVAL;
     Rotate a = rotation_of(how, positions, rows);
@@ -166,6 +175,8 @@ int gemv_norm_rotate_append(const gemv_rotation* how, const gemv_heads* q, const
         return GEMV_E_UNSUPPORTED;
     if (rows == 0)
         return GEMV_OK;
+    if (!laid_alike(q, dtype, cache->dtype))
+        return GEMV_E_INVAL;
     if (positions == nullptr || slots == nullptr || (how->rotated > 0 && how->freqs == nullptr) ||
         (cache->pages > 0 && (cache->k == nullptr || cache->v == nullptr)))
         return GEMV_E_INVAL;

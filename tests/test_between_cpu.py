@@ -39,7 +39,7 @@ def _how(**kw):
 
 
 def _heads(heads=2, **kw):
-    return _of(binding.Heads, dict(x=P, stride=64 * max(heads, 0), heads=heads, weight=P, out=P, out_stride=64 * max(heads, 0)), kw)
+    return _of(binding.Heads, dict(x=P, stride=64 * max(heads, 0), heads=heads, weight=P, out=2 * P, out_stride=64 * max(heads, 0)), kw)
 
 
 def _turn(lib, how=None, q=None, k=None, dtype=1, out_dtype=1, positions=P, rows=2):
@@ -61,6 +61,8 @@ def test_rotation_status(lib, call):
     for kw in (dict(q=_heads(-1)), dict(q=_heads(4, stride=255)), dict(q=_heads(4, x=None)), dict(q=_heads(4, out=None)),
                dict(q=_heads(4, out_stride=255)), dict(k=_heads(2, stride=100)), dict(k=_heads(2, x=None)), dict(dtype=3), dict(dtype=-1),
                dict(positions=None), dict(rows=-1)):
+        assert call(lib, **kw) == INVAL, kw
+    for kw in (dict(q=_heads(4, out=P + 64, x=P + 64, out_stride=264)), dict(q=_heads(4, out=P + 64, x=P + 64), dtype=0)):
         assert call(lib, **kw) == INVAL, kw
     assert call(lib, rows=0, positions=None, q=_heads(4, x=None, out=None)) == OK
 

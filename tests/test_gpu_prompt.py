@@ -59,7 +59,7 @@ def test_counts(gpu, n, old, dtype):
 
 
 @pytest.mark.parametrize("dtype", HALVES, ids=str)
-@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("page", [16, 24, 5])
 @pytest.mark.parametrize("dim", [8, 16, 40, 64, 72, 80, 96, 104, 120, 128, 136, 192, 248, 256])
 def test_head_sizes(gpu, dim, page, dtype):
     _check(ref.Pool([70, 3, 129], 2, dim, page, dtype, seed=dim), [66, 2, 40], 6, f"dim {dim} page {page} {dtype}")
@@ -74,6 +74,33 @@ def test_head_groups(gpu, heads, kv):
 @pytest.mark.parametrize("layout", ["slots", "heads", "padded"])
 def test_pages_and_layouts(gpu, page, layout):
     _check(ref.Pool([90, 2, 200], 2, 64, page, torch.bfloat16, seed=page, layout=layout), [90, 2, 33], 4, f"page {page} {layout}")
+
+
+@pytest.mark.parametrize("kv", [1, 3, 4, 8, 16, 24])
+def test_every_order_of_workgroups(gpu, kv):
+    # sets of workgroups that are a multiple of eight, and others; one part of the keys and several
+    for lens, news in (([333, 150], [333, 150]), ([2000, 1300], [5, 3])):
+        _check(ref.Pool(lens, kv, 64, 16, seed=kv), news, 2 * kv, f"{kv} heads, {news}")
+
+
+def test_long_prompts(gpu):
+    """20000 slots, 2500 new tokens; a sample of rows against the plain form."""
+    pool = ref.Pool([20000], 1, 128, 16, torch.bfloat16, seed=31)
+    q = _query(2500, 4, 128, torch.bfloat16, 31)
+    cache = binding.PagedCache(pool.dk, pool.dv)
+    starts = torch.tensor([0, 2500], dtype=torch.int32, device="cuda")
+    k, _ = ref.gathered(pool, pool.k, 0, 20000)
+    v, _ = ref.gathered(pool, pool.v, 0, 20000)
+    sample = np.array([0, 1, 31, 32, 63, 64, 100, 1023, 1024, 1700, 2047, 2400, 2498, 2499])
+    half, low = pref._power_errors(torch.bfloat16)
+    for window, sinks in ((None, 0), (4096, 4), (1000, 0)):
+        say(f"[prompt] 2500 of 20000, window {window}")
+        got = binding.prompt_attention(cache, pool.dtable, pool.dlens, starts, q.cuda(), window=window, sinks=sinks).cpu()
+        sees = pref.seen(2500, 20000, window, sinks)[sample]
+        for h in range(4):
+            want, bound = pref.attend(k[0], v[0], q[sample, h].double().numpy(), sees, 128 ** -0.5, np.full(20000, half), low)
+            off = np.abs(got[sample, h].double().numpy() - want)
+            assert np.all(off <= pref.stored(want, bound, torch.bfloat16)), (window, h)
 
 
 def test_ragged_batch_with_empty_sequences(gpu):
@@ -226,13 +253,13 @@ def test_rising_logits(gpu):
 
 
 @pytest.mark.parametrize("dtype", HALVES, ids=str)
-@pytest.mark.parametrize("page", [16, 5])
-def test_what_a_row_does_not_see_does_not_touch_it(gpu, page, dtype):
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 24), (64, 5), (96, 16), (128, 16), (200, 16), (256, 16)])
+def test_what_a_row_does_not_see_does_not_touch_it(gpu, dim, page, dtype):
     # NaN and infinities in keys and values of later tokens, and of those before the window
     lens, news = [200, 150], [150, 150]
     for window, sinks in ((None, 0), (40, 2)):
-        pool = ref.Pool(lens, 1, 64, page, dtype, seed=12)
-        q = _query(300, 2, 64, dtype, 12)
+        pool = ref.Pool(lens, 1, dim, page, dtype, seed=12)
+        q = _query(300, 2, dim, dtype, 12)
         bad = {0: (60, 100, 199), 1: (0, 33, 149)}
         for b, slots in bad.items():
             for i, j in enumerate(slots):
@@ -243,7 +270,7 @@ def test_what_a_row_does_not_see_does_not_touch_it(gpu, page, dtype):
         cache = binding.PagedCache(pool.dk, pool.dv)
         out = binding.prompt_attention(cache, pool.dtable, pool.dlens, torch.tensor([0, 150, 300], dtype=torch.int32, device="cuda"),
                                        q.cuda(), window=window, sinks=sinks).cpu().double().numpy()
-        want, bound, _ = pref.prompt(pool, q, [0, 150, 300], 0.125, window, sinks)   # of the finite pool
+        want, bound, _ = pref.prompt(pool, q, [0, 150, 300], dim ** -0.5, window, sinks)   # of the finite pool
         for b in range(2):
             sees = pref.seen(150, lens[b], window, sinks)
             for t in range(150):
@@ -252,7 +279,7 @@ def test_what_a_row_does_not_see_does_not_touch_it(gpu, page, dtype):
                 if nan_key:
                     assert np.all(np.isnan(row)), (b, t)
                     continue
-                cols = np.zeros(64, bool)
+                cols = np.zeros(dim, bool)
                 for i, j in enumerate(bad[b]):
                     if sees[t, j]:
                         cols[i::7] = True

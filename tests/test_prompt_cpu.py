@@ -65,6 +65,14 @@ def test_call_status(lib):
     for kw in (dict(rows=0, q=None, out=None), dict(max_new=0)):
         assert _prompt(lib, c, b, **kw) == OK, kw
     assert _prefix(lib, c, b, starts=None) == INVAL
+    most = (1 << 31) - 1
+    one = _cache(heads=1, stride_slot=64)
+    assert _prompt(lib, one, b, rows=most, q_stride=most * 64 // 8 * 8 + 64, heads=most) == UNSUPPORTED
+    assert _prompt(lib, c, _batch(batch=most), rows=8) == UNSUPPORTED
+    assert _prefix(lib, one, b, q_stride=most * 64 // 8 * 8 + 64, heads=most) == UNSUPPORTED
+    assert _prefix(lib, c, _batch(batch=most)) == UNSUPPORTED
+    assert _prefix(lib, c, b, far=_batch(batch=most)) == UNSUPPORTED
+    assert lib.gemv_prompt_attention_workspace(ctypes.byref(one), ctypes.byref(b), most, 4, most, 0, 0) == 0
     assert lib.gemv_prompt_attention_workspace(None, None, 8, 4, 4, 0, 0) == 0
     assert lib.gemv_prefix_attention_workspace(None, None, None, 4) == 0
     for bad in ((-1, 4, 4, 0, 0), (8, -1, 4, 0, 0), (8, 4, 3, 0, 0), (8, 4, 4, -1, 0), (8, 4, 4, 0, -1)):
