@@ -18,7 +18,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // parts of the keys and tiles of keys in each.
 struct Tiling {
     int64_t tiles;
-    int parts, chunk;
+    TileOrder order;
+    int laps, run, parts, chunk;
     size_t ms_at, out_at, bytes;
 };
 
@@ -40,6 +41,27 @@ Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int
     constexpr double kStart = 1.5, kJoin = 4.0, kMoved = 6e6, kPart = 0.06, kWave = 3.5 / 8192;
     Tiling t{};
     t.tiles = rows * group / kTileRows + batch;
+    t.order = kTogether;
+    t.laps = 1;
+    t.run = (int)t.tiles;
+    // Runs of 8 of the last tiles, where sequences have two runs and not much fewer
+    // places hold them all: 6 x 1999 tokens, 16 heads of 64, 58 us (68 a sequence
+    // after the other, 57 in runs of 1), 4 x 8192 of them 501 (537, 590), 2 x 8192,
+    // 32/8 heads of 128, 640 (632, 985: keys of both sequences are more than the L2),
+    // 40 x 300 79 (73, 74).
+    const int64_t even = ((int64_t)(max_new > 0 ? max_new : rows) * group + kTileRows - 1) / kTileRows;
+    if (even == 1) {
+        // a tile each: parts of one sequence after another, of which the last are short
+        // (20 x 5 tokens through a window of 2000: 35 us, 49 part after part)
+        t.order = kSingle;
+        t.tiles = batch;
+        t.run = 1;
+    } else if (even >= 16 && even * batch <= 2 * t.tiles) {
+        t.order = kLaps;
+        t.tiles = even;
+        t.laps = batch;
+        t.run = 8;
+    }
     int64_t keys = ((int64_t)limit + kTileKeys - 1) / kTileKeys;
     if (window > 0) {
         const int64_t near = ((int64_t)window + kTileRows / group + kTileKeys) / kTileKeys + 1;
@@ -233,6 +255,10 @@ Prompt tiled(const gemv_kv_cache* c, const Pages& at, int batch, const int32_t* 
     a.group = q_heads / c->heads;
     a.group_of = divider(a.group);
     a.tiles = (int)t.tiles;
+    a.order = t.order;
+    a.laps = t.laps;
+    a.run = t.run;
+    a.stretch = t.run * t.laps;
     a.parts = t.parts;
     a.chunk = t.chunk;
     const float size = fabsf(scale) * kLog2e;
@@ -397,7 +423,7 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
         j.from[0] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
         return join_parts(j, cache->dtype, dev.cus, stream);
     }
-    const int64_t grid = p.tiling.tiles * cache->heads * p.tiling.parts;
+    const int64_t grid = p.tiling.tiles * p.tiling.laps * cache->heads * p.tiling.parts;
     const int block = 256 * outputs_of(cache->head_dim);
     if (!fits(grid, block))
         return GEMV_E_UNSUPPORTED;
@@ -456,7 +482,7 @@ int gemv_prefix_attention(const gemv_kv_cache* cache, const gemv_kv_batch* prefi
     const PrefixPlan p = plan_prefix(cache, prefixes, batch, far.limit, at.limit, q_heads, dev.cus);
     if (!holds(workspace, workspace_bytes, p.bytes))
         return GEMV_E_INVAL;
-    const int64_t far_count = p.shared.tiles * cache->heads * p.shared.parts, far_blocks = (far_count + 7) / 8 * 8;
+    const int64_t far_count = p.shared.tiles * p.shared.laps * cache->heads * p.shared.parts, far_blocks = (far_count + 7) / 8 * 8;
     const int64_t near_count = p.own.parts > 0 ? newest_grid(cache, batch->batch, p.own) : 0;
     const int block = 256 * outputs_of(cache->head_dim);
     if (!fits(far_blocks + near_count, block) || !joins_fit(batch->batch, q_heads))

@@ -32,6 +32,13 @@ constexpr int outputs_of(int dim) { return dim > 128 ? 2 : 1; }
 // tokens of 16 heads: 79.9 -> 69.1 us; a fourth leaves too few registers, 83.2).
 constexpr int waves_of(int dim) { return dim > 64 ? 2 : 3; }
 
+// Where the row tiles stand among a head's places.
+enum TileOrder {
+    kTogether,               // rows * group / 128 + batch places for all sequences' tiles in turn
+    kSingle,                 // no sequence has more than one: place i is sequence i's
+    kLaps,                   // as many places for each sequence, `run` of one before the next one's
+};
+
 struct Prompt {
     Pages at;
     const uint16_t* k;
@@ -46,7 +53,10 @@ struct Prompt {
     bool causal;
     int window;              // tokens seen, the row's own included; 0: all
     int sinks, sink_tiles;   // first tokens seen all the same, and the tiles that hold them
-    int tiles;               // places for row tiles per key-value head: rows * group / 128 + batch
+    TileOrder order;
+    int tiles;               // places for row tiles per key-value head: of all sequences, or kLaps of each
+    int laps;                // 1, kLaps: batch
+    int run, stretch;        // places that follow each other, and of all laps: run * laps
     int parts, chunk;        // workgroups over the keys, and tiles of keys of each
     float scale;             // of the logits, above zero, log2(e) included
     float slack;             // kSlack / scale
@@ -238,28 +248,40 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
     const int half = lane >> 5;
 
     // Workgroups go to the eight XCDs in turn.  Those that read the same keys
-    // (a head's, of a part) follow each other on one XCD where such sets are a
-    // multiple of eight; the last rows, which see most, come first, and the last
-    // parts, which only long sequences have.  From part to part an XCD moves on by a head, so that it sees every head's part of the
-    // address space.
+    // (a head's, of a part) are on one XCD where such sets are a multiple of
+    // eight, and the last parts, which only long sequences have, come first.  From
+    // part to part an XCD moves on by a head, so that it sees every head's part of
+    // the address space.  Of the row tiles the last, which see most, come first, a run
+    // of them from one sequence before the next one's, so that they find its keys
+    // in the L2, and all sequences' and sets' last run before the one before it, so
+    // that what is started last is short.
     const int sets = a.heads * a.parts;
     // `one`: the same for all lanes, and known to be where the vector unit has computed it
     auto one = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
     auto quotient = [&](int x, int y) { return one((int)((unsigned)x / (unsigned)y)); };
-    int set, place;
-    if (sets % 8 == 0) {
-        const int j = block >> 3, m = quotient(j, a.tiles);
-        set = m * 8 + (block & 7);
-        place = j - m * a.tiles;
-    } else {
-        place = quotient(block, sets);
-        set = block - place * sets;
-    }
+    const bool eight = sets % 8 == 0;
+    const int each = eight ? sets >> 3 : 1;                                     // sets of an XCD
+    int j = eight ? block >> 3 : quotient(block, sets);
+    const int first = quotient(j, each * a.stretch);
+    j -= first * each * a.stretch;
+    const int left = a.tiles - first * a.run;
+    const int run = left < a.run ? left : a.run;
+    const int lap = quotient(j, run), set_of = quotient(lap, a.laps);
+    const int set = eight ? set_of * 8 + (block & 7) : block - quotient(block, sets) * sets;
+    const int place = a.tiles - 1 - first * a.run - (j - lap * run);
     const int part_back = quotient(set, a.heads), part = a.parts - 1 - part_back;
     const int kv_at = set - part_back * a.heads + part;
     const int kv = kv_at - quotient(kv_at, a.heads) * a.heads;
-    place = a.tiles - 1 - place;
-    const Sequence sequence = sequence_at(a.at, a.starts, a.batch, a.rows, a.group, place);
+    Sequence sequence;
+    int tile = place;
+    if (a.order != kTogether) {
+        const int at = a.order == kSingle ? place : lap - set_of * a.laps;
+        tile = a.order == kSingle ? 0 : place;
+        sequence = Sequence{at, a.at.length(at), row_start(a.starts, at, a.rows), row_start(a.starts, at + 1, a.rows)};
+    } else {
+        sequence = sequence_at(a.at, a.starts, a.batch, a.rows, a.group, place);
+        tile = place - (int)(sequence.from * a.group / kTileRows) - sequence.b;
+    }
     const int b = one(sequence.b), len = one(sequence.len);
     const int64_t from = sequence.from, to = sequence.to;
     int64_t n64 = to - from;
@@ -267,7 +289,7 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
     const int n = one((int)n64);                     // new tokens
     const int64_t row0 = to - n64;                                              // the first of them
     // this tile's first row; rows times the group are below 2^30, as the launch's work-items are
-    const int r0 = one((int)(place - from * a.group / kTileRows - b) * kTileRows);
+    const int r0 = one(tile * kTileRows);
     if (n <= 0 || r0 < 0 || r0 >= n * a.group)
         return;
     const int rows = n * a.group - r0 < kTileRows ? n * a.group - r0 : kTileRows;

@@ -83,6 +83,14 @@ def test_every_order_of_workgroups(gpu, kv):
         _check(ref.Pool(lens, kv, 64, 16, seed=kv), news, 2 * kv, f"{kv} heads, {news}")
 
 
+@pytest.mark.parametrize("kv", [1, 5, 8])
+@pytest.mark.parametrize("news", [[300, 290, 137, 299], [310, 0, 300], [300, 3, 1, 0]], ids=str)
+def test_row_tiles_in_runs(gpu, kv, news):
+    # seventeen row tiles and fewer, of alike and of unlike sequences, one part of the keys and several
+    for old in (0, 900):
+        _check(ref.Pool([n + old for n in news], kv, 64, 16, seed=kv), news, 7 * kv, f"{kv} heads, {news} after {old}")
+
+
 def test_long_prompts(gpu):
     """20000 slots, 2500 new tokens; a sample of rows against the plain form."""
     pool = ref.Pool([20000], 1, 128, 16, torch.bfloat16, seed=31)
