@@ -20,6 +20,7 @@ struct Tiling {
     int64_t tiles;
     TileOrder order;
     int laps, run, parts, chunk;
+    int64_t places;          // workgroups of a key-value head
     size_t ms_at, out_at, bytes;
 };
 
@@ -36,7 +37,7 @@ struct Tiling {
 // us, 91 without).  `per_cu`: workgroups that a CU holds (two, for heads up to
 // 128, three up to 64), or that it takes of these beside others.
 Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int limit, int window, int sinks, int max_new,
-                 double per_cu, int cus)
+                 double per_cu, bool shares, int cus)
 {
     constexpr double kStart = 1.5, kJoin = 4.0, kMoved = 6e6, kPart = 0.06, kWave = 3.5 / 8192;
     Tiling t{};
@@ -91,6 +92,14 @@ Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int
             t.parts = (int)parts;
             t.chunk = (int)chunk;
         }
+    }
+    t.places = t.tiles * t.laps * t.parts;
+    // A tile each, in several parts: as many places, shared out by the lengths, which
+    // only the device knows; a long sequence takes up to four times the parts.
+    if (shares && t.order == kSingle && t.parts > 1 && batch > 1 && batch <= 64 && window == 0) {
+        t.order = kShares;
+        t.tiles = t.places;
+        t.parts = (int)(t.places < 4 * t.parts ? t.places : 4 * t.parts);
     }
     return t;
 }
@@ -297,7 +306,7 @@ Plan plan_prompt(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit, int 
         return p;
     }
     p.tiling = tile_rows(c, rows, s->batch, q_heads / c->heads, limit, p.window, p.sinks,
-                         max_new < rows ? max_new : rows, 2.0, cus);
+                         max_new < rows ? max_new : rows, 2.0, true, cus);
     p.joined = p.tiling.parts > 1;
     place_parts(&p.tiling, 0, heads, c->head_dim, p.joined);
     p.bytes = p.tiling.bytes;
@@ -317,9 +326,9 @@ PrefixPlan plan_prefix(const gemv_kv_cache* c, const gemv_kv_batch* prefixes, co
     const int64_t heads = (int64_t)s->batch * q_heads;
     // one place and a half: the others are for the sequences' own tokens (128 sequences
     // behind two prefixes of up to 32768: 118 us with 12 parts, 127 with 16, 140 with 8)
-    p.shared = tile_rows(c, s->batch, prefixes->batch, q_heads / c->heads, far_limit, 0, 0, 0, 1.5, cus);
+    p.shared = tile_rows(c, s->batch, prefixes->batch, q_heads / c->heads, far_limit, 0, 0, 0, 1.5, false, cus);
     if (prefixes->batch == 0 || far_limit == 0)
-        p.shared.parts = 0;
+        p.shared.parts = 0, p.shared.places = 0;
     place_parts(&p.shared, 0, heads, c->head_dim, true);
     p.own = split_for(c, s, limit, q_heads, false, cus, false);
     if (limit == 0)
@@ -423,7 +432,7 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
         j.from[0] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
         return join_parts(j, cache->dtype, dev.cus, stream);
     }
-    const int64_t grid = p.tiling.tiles * p.tiling.laps * cache->heads * p.tiling.parts;
+    const int64_t grid = p.tiling.places * cache->heads;
     const int block = 256 * outputs_of(cache->head_dim);
     if (!fits(grid, block))
         return GEMV_E_UNSUPPORTED;
@@ -482,7 +491,7 @@ int gemv_prefix_attention(const gemv_kv_cache* cache, const gemv_kv_batch* prefi
     const PrefixPlan p = plan_prefix(cache, prefixes, batch, far.limit, at.limit, q_heads, dev.cus);
     if (!holds(workspace, workspace_bytes, p.bytes))
         return GEMV_E_INVAL;
-    const int64_t far_count = p.shared.tiles * p.shared.laps * cache->heads * p.shared.parts, far_blocks = (far_count + 7) / 8 * 8;
+    const int64_t far_count = p.shared.places * cache->heads, far_blocks = (far_count + 7) / 8 * 8;
     const int64_t near_count = p.own.parts > 0 ? newest_grid(cache, batch->batch, p.own) : 0;
     const int block = 256 * outputs_of(cache->head_dim);
     if (!fits(far_blocks + near_count, block) || !joins_fit(batch->batch, q_heads))

@@ -37,6 +37,7 @@ enum TileOrder {
     kTogether,               // rows * group / 128 + batch places for all sequences' tiles in turn
     kSingle,                 // no sequence has more than one: place i is sequence i's
     kLaps,                   // as many places for each sequence, `run` of one before the next one's
+    kShares,                 // none has more than one: `tiles` places for the parts of all, shared out by their lengths
 };
 
 struct Prompt {
@@ -57,7 +58,7 @@ struct Prompt {
     int tiles;               // places for row tiles per key-value head: of all sequences, or kLaps of each
     int laps;                // 1, kLaps: batch
     int run, stretch;        // places that follow each other, and of all laps: run * laps
-    int parts, chunk;        // workgroups over the keys, and tiles of keys of each
+    int parts, chunk;        // workgroups over the keys, and tiles of keys of each; kShares: parts at the most
     float scale;             // of the logits, above zero, log2(e) included
     float slack;             // kSlack / scale
     unsigned keep, flip;     // bits of q: none where the scale is zero; the signs flipped where it is negative
@@ -165,8 +166,7 @@ __device__ __forceinline__ unsigned bits_below(int64_t n) { return n <= 0 ? 0u :
 // 64 is loaded at once, for each load that waits for another is half a
 // microsecond of a workgroup's start.
 struct Sequence {
-    int b, len;
-    int64_t from, to;   // its rows
+    int b, len, from, to;   // its rows
 };
 
 __device__ __forceinline__ Sequence sequence_at(const Pages& at, const int32_t* starts, int batch, int rows, int group, int64_t u)
@@ -188,6 +188,57 @@ __device__ __forceinline__ Sequence sequence_at(const Pages& at, const int32_t* 
     const int it = n > 0 ? n - 1 : 0;
     return Sequence{low + it, __builtin_amdgcn_readlane(len, it), __builtin_amdgcn_readlane(from, it),
                     __builtin_amdgcn_readlane(to, it)};
+}
+
+// Place `w` of kShares: every part is of `chunk` tiles of keys, about the fewest
+// with which the places hold all sequences' parts, so that short sequences leave
+// no place idle (4 x 6 tokens behind up to 20000, 16/4 heads of 256: 74 -> 63 us;
+// 4 x 7 behind up to 65536, 32/8 heads of 128: 149 -> 136).  Lane b counts for
+// sequence b.
+struct Share {
+    Sequence sequence;
+    int part, parts, chunk;   // parts: of this sequence; 0: nobody's place
+};
+
+__device__ __forceinline__ Share share_at(const Prompt& a, int w)
+{
+    const int lane = threadIdx.x & 63;
+    const int b = lane < a.batch ? lane : a.batch - 1;
+    const int from = (int)row_start(a.starts, b, a.rows), to = (int)row_start(a.starts, b + 1, a.rows), len = a.at.length(b);
+    const bool any = lane < a.batch && to > from;
+    const int count = any && len > 0 ? (len - 1) / kTileKeys + 1 : any;   // a sequence without keys has its rows cleared
+    int most = count;
+    unsigned all = count;   // no more than 64 times 2^25
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int other = __shfl_xor(most, d);
+        most = most > other ? most : other;
+        all += (unsigned)__shfl_xor((int)all, d);
+    }
+    // with fewer neither the places nor the room for parts would do
+    int chunk = (int)((all + a.tiles - 1) / a.tiles);
+    const int for_room = (most + a.parts - 1) / a.parts;
+    chunk = chunk > for_room ? chunk : for_room;
+    chunk = chunk > 1 ? chunk : 1;
+    int parts, upto, held;
+    for (;; chunk += (chunk + 7) / 8) {   // ends: there is a place for each sequence
+        parts = (count + chunk - 1) / chunk;
+        upto = parts;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(upto, d);
+            upto += lane >= d ? up : 0;
+        }
+        held = __builtin_amdgcn_readlane(upto, 63);
+        if (held <= a.tiles || chunk >= most)
+            break;
+    }
+    if (w >= held)
+        return Share{};
+    const int it = __popcll(__ballot(upto <= w)), own = __builtin_amdgcn_readlane(parts, it);
+    return Share{Sequence{it, __builtin_amdgcn_readlane(len, it), __builtin_amdgcn_readlane(from, it),
+                          __builtin_amdgcn_readlane(to, it)},
+                 w - __builtin_amdgcn_readlane(upto, it) + own, own, chunk};
 }
 
 // 16 zeros that slots without a page are read from
@@ -259,35 +310,53 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
     // `one`: the same for all lanes, and known to be where the vector unit has computed it
     auto one = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
     auto quotient = [&](int x, int y) { return one((int)((unsigned)x / (unsigned)y)); };
-    const bool eight = sets % 8 == 0;
-    const int each = eight ? sets >> 3 : 1;                                     // sets of an XCD
-    int j = eight ? block >> 3 : quotient(block, sets);
-    const int first = quotient(j, each * a.stretch);
-    j -= first * each * a.stretch;
-    const int left = a.tiles - first * a.run;
-    const int run = left < a.run ? left : a.run;
-    const int lap = quotient(j, run), set_of = quotient(lap, a.laps);
-    const int set = eight ? set_of * 8 + (block & 7) : block - quotient(block, sets) * sets;
-    const int place = a.tiles - 1 - first * a.run - (j - lap * run);
-    const int part_back = quotient(set, a.heads), part = a.parts - 1 - part_back;
-    const int kv_at = set - part_back * a.heads + part;
-    const int kv = kv_at - quotient(kv_at, a.heads) * a.heads;
     Sequence sequence;
-    int tile = place;
-    if (a.order != kTogether) {
-        const int at = a.order == kSingle ? place : lap - set_of * a.laps;
-        tile = a.order == kSingle ? 0 : place;
-        sequence = Sequence{at, a.at.length(at), row_start(a.starts, at, a.rows), row_start(a.starts, at + 1, a.rows)};
+    int kv, tile, part, parts = a.parts, chunk = a.chunk;
+    if (a.order == kShares) {
+        const int w = quotient(block, a.heads);
+        const Share share = share_at(a, w);
+        if (share.parts == 0)
+            return;
+        sequence = share.sequence;
+        tile = 0;
+        part = share.part;
+        parts = share.parts;
+        chunk = share.chunk;
+        const int kv_at = block - w * a.heads + part;
+        kv = kv_at - quotient(kv_at, a.heads) * a.heads;
     } else {
-        sequence = sequence_at(a.at, a.starts, a.batch, a.rows, a.group, place);
-        tile = place - (int)(sequence.from * a.group / kTileRows) - sequence.b;
+        const bool eight = sets % 8 == 0;
+        const int each = eight ? sets >> 3 : 1;                                 // sets of an XCD
+        int j = eight ? block >> 3 : quotient(block, sets);
+        const int first = quotient(j, each * a.stretch);
+        j -= first * each * a.stretch;
+        const int left = a.tiles - first * a.run;
+        const int run = left < a.run ? left : a.run;
+        const int lap = quotient(j, run), set_of = quotient(lap, a.laps);
+        const int set = eight ? set_of * 8 + (block & 7) : block - quotient(block, sets) * sets;
+        const int place = a.tiles - 1 - first * a.run - (j - lap * run);
+        const int part_back = quotient(set, a.heads);
+        part = a.parts - 1 - part_back;
+        const int kv_at = set - part_back * a.heads + part;
+        kv = kv_at - quotient(kv_at, a.heads) * a.heads;
+        tile = place;
+        if (a.order != kTogether) {
+            const int at = a.order == kSingle ? place : lap - set_of * a.laps;
+            tile = a.order == kSingle ? 0 : place;
+            sequence = Sequence{at, a.at.length(at), (int)row_start(a.starts, at, a.rows), (int)row_start(a.starts, at + 1, a.rows)};
+        } else {
+            sequence = sequence_at(a.at, a.starts, a.batch, a.rows, a.group, place);
+            tile = place - (int)((int64_t)sequence.from * a.group / kTileRows) - sequence.b;
+        }
     }
-    const int b = one(sequence.b), len = one(sequence.len);
-    const int64_t from = sequence.from, to = sequence.to;
-    int64_t n64 = to - from;
-    n64 = n64 < a.max_new ? n64 : a.max_new;
-    const int n = one((int)n64);                     // new tokens
-    const int64_t row0 = to - n64;                                              // the first of them
+    kv = one(kv);
+    part = one(part);
+    parts = one(parts);
+    chunk = one(chunk);
+    const int b = one(sequence.b), len = one(sequence.len), to = one(sequence.to);
+    int n = to - one(sequence.from);                                            // new tokens
+    n = n < a.max_new ? n : a.max_new;
+    const int64_t row0 = to - n;                                                // the first of them
     // this tile's first row; rows times the group are below 2^30, as the launch's work-items are
     const int r0 = one(tile * kTileRows);
     if (n <= 0 || r0 < 0 || r0 >= n * a.group)
@@ -313,7 +382,7 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
         jump = jump > 0 ? jump : 0;
     }
     const int count = tiles_all - jump;
-    const int begin = part * a.chunk, end = count < begin + a.chunk ? count : begin + a.chunk;
+    const int begin = part * chunk, end = count < begin + chunk ? count : begin + chunk;
     auto slot_of = [&](int u) { return (u < a.sink_tiles ? u : u + jump) * kTileKeys; };
 
     // this lane's query row
@@ -642,6 +711,12 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
         if (half == 0 && output == 0) {
             a.part_ms[to_part * 2] = m == -kInf ? -kInf : m * a.scale;
             a.part_ms[to_part * 2 + 1] = sum;
+            // parts that this sequence does not have saw nothing
+            if (a.order == kShares)
+                for (int p = parts + part; p < a.parts; p += parts) {
+                    a.part_ms[(at * a.parts + p) * 2] = -kInf;
+                    a.part_ms[(at * a.parts + p) * 2 + 1] = 0.0f;
+                }
         }
         if (begin < end)
 #pragma unroll

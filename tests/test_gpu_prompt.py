@@ -91,6 +91,21 @@ def test_row_tiles_in_runs(gpu, kv, news):
         _check(ref.Pool([n + old for n in news], kv, 64, 16, seed=kv), news, 7 * kv, f"{kv} heads, {news} after {old}")
 
 
+@pytest.mark.parametrize("lens,news", [
+    ([0, 5000, 3, 700, 64, 1], [2, 3, 3, 0, 1, 1]),
+    ([9000, 65, 64, 63], [4, 2, 0, 4]),
+    ([1, 1, 0, 2], [1, 2, 3, 0]),
+    ([(i * 131) % 1700 for i in range(64)], [i % 4 for i in range(64)]),
+    ([(i * 131) % 700 for i in range(65)], [i % 4 for i in range(65)]),
+], ids=["empty", "one long", "short", "64", "65"])
+@pytest.mark.parametrize("kv,dim", [(1, 64), (3, 256), (8, 128)])
+def test_few_new_tokens_of_unlike_sequences(gpu, lens, news, kv, dim):
+    # tables with room for 9000 slots whatever the lengths are: several parts of the keys, shared out by the lengths
+    pool = ref.Pool(lens, kv, dim, 16, torch.bfloat16, seed=kv)
+    pool.dtable = torch.cat([pool.dtable, pool.dtable[:, :1].expand(-1, 563 - pool.width)], 1).contiguous()
+    _check(pool, news, 4 * kv, f"{kv} heads of {dim}, {news}", before=1, after=2, max_new=max(news))
+
+
 def test_long_prompts(gpu):
     """20000 slots, 2500 new tokens; a sample of rows against the plain form."""
     pool = ref.Pool([20000], 1, 128, 16, torch.bfloat16, seed=31)
