@@ -29,8 +29,8 @@ struct Tiling {
 // holds two workgroups (one for heads over 128), less where it holds one.  As
 // many as there are places for start together, and where they see alike the next
 // ones wait for them: a round that is half empty costs as much as a full one
-// (4 x 7 tokens over 65543 keys: 16 parts, one round, 148 us; 20 parts 170, 32
-// parts 155).  Where a sequence's newest tokens are most of it they see fewer keys
+// (4 x 7 tokens over 65543 keys in parts alike: 16 parts, one round, 149 us; 24
+// parts 163, 32 parts 161).  Where a sequence's newest tokens are most of it they see fewer keys
 // the earlier they are, and the work spreads evenly but for its end.  A join
 // costs a launch, its parts written and read at 6 TB/s, kPart for each of a row's,
 // and its waves: 8192 at a time for 3.5 us (7943 rows of 16 heads in two parts: 155

@@ -29,7 +29,8 @@ constexpr int outputs_of(int dim) { return dim > 128 ? 2 : 1; }
 
 // Waves of a SIMD that registers are shared out for.  Heads of 64 have as many
 // exponentials for half the matrix products and gain by a third wave (6 x 1999
-// tokens of 16 heads: 79.9 -> 69.1 us; a fourth leaves too few registers, 83.2).
+// tokens of 16 heads, one sequence's tiles after another's: 79.9 -> 69.1 us; a
+// fourth leaves too few registers, 83.2).
 constexpr int waves_of(int dim) { return dim > 64 ? 2 : 3; }
 
 // Where the row tiles stand among a head's places.
@@ -192,7 +193,7 @@ __device__ __forceinline__ Sequence sequence_at(const Pages& at, const int32_t* 
 
 // Place `w` of kShares: every part is of `chunk` tiles of keys, about the fewest
 // with which the places hold all sequences' parts, so that short sequences leave
-// no place idle (4 x 6 tokens behind up to 20000, 16/4 heads of 256: 74 -> 63 us;
+// no place idle (4 x 6 tokens behind up to 20000, 16/4 heads of 256: 74 -> 65 us;
 // 4 x 7 behind up to 65536, 32/8 heads of 128: 149 -> 136).  Lane b counts for
 // sequence b.
 struct Share {
@@ -265,8 +266,17 @@ __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 //
 // RUN: slots that lie in one page from their first multiple on, 16 or 8, whose
 // address is the same for all lanes; 1: each row has an address of its own (4 x
-// 8192 tokens, 16 heads of 64: 586 us in pages of 16, 617 in pages of 24, 682 with
-// an address for each row).
+// 8192 tokens, 16 heads of 64: 513 us in pages of 16, 517 in pages of 24, 562 in
+// pages of 5; 2 x 8192, 32/8 heads of 128: 610, 633, 736).
+//
+// Bound, where prompts are long, by the matrix and the vector units in turn: both
+// are busy 45 % of the time and a SIMD's two waves only partly overlap, for all
+// wait for each tile of keys at one barrier (2 x 16384 tokens through a window of
+// 4096, 32/8 heads of 128: 1706 us, 959 TFLOP/s; the products and barriers alone
+// take 64 % of a long prompt's time, exponentials 10 %, reads of LDS 16 %, loads
+// 17 %, the maximum 3 %, each taken out by itself).  Where rows are few, by memory: 4 x
+// 7 tokens behind up to 65536 read 715 MB in 131 us.  Of a few hundred rows, by the
+// 1.1 to 2 us that a step takes however few waves there are.
 //
 // Places in LDS: piece c (16 bytes) of key row r lies at c ^ swizzle(r), such
 // that the 16 rows that a read of keys takes at a time, and the four rows of
@@ -758,7 +768,9 @@ prompt_kernel(Prompt a)
 // Shared prefixes and the sequences' own tokens in one launch: the first
 // `far_blocks` workgroups (a multiple of eight, so that the others too keep to
 // their XCDs) take the prefixes, which the matrix units bound, the others the
-// rest, which memory does; a CU that holds one of each is slowed by neither.
+// rest, which memory does; a CU that holds one of each is slowed by neither (128
+// sequences behind two prefixes of up to 32768, 32/8 heads of 128: 146 us in two
+// launches, 110 in one, and 9 for the join).
 template <int DT, int DP, int RUN, bool EXACT>
 __global__ void __launch_bounds__(256 * outputs_of(DP), waves_of(DP))
 prefix_kernel(Prompt far, Attention near, int far_blocks, int far_count)
@@ -774,7 +786,6 @@ prefix_kernel(Prompt far, Attention near, int far_blocks, int far_count)
     else if (block < far_count)
         prompt_block<DT, DP, RUN, EXACT>(far, block, shared.far);
 }
-
 // Parts of the same rows: of `parts` each, in the layout of part_out and
 // part_ms.  `starts`: the groups whose rows the parts are of (a row outside
 // them has none), or null: every row.
@@ -895,7 +906,8 @@ __device__ __forceinline__ void join_row(const Join& a, int64_t at, const int (&
 
 constexpr int kJoinWaves = 4;
 
-// A wave for each row's head, or (SPREAD) all four where there are few rows.
+// A wave for each row's head, or (SPREAD) all four where there are few rows.  Bound
+// by latency: 4 to 6 us for up to a thousand rows' heads, 9 for 4096 of a dozen parts.
 template <int DT, bool SPREAD>
 __global__ void __launch_bounds__(kJoinWaves * 64)
 join_parts_kernel(Join a)
