@@ -45,11 +45,11 @@ Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int
     t.order = kTogether;
     t.laps = 1;
     t.run = (int)t.tiles;
-    // Runs of 8 of the last tiles, where sequences have two runs and not much fewer
-    // places hold them all: 6 x 1999 tokens, 16 heads of 64, 58 us (68 a sequence
-    // after the other, 57 in runs of 1), 4 x 8192 of them 501 (537, 590), 2 x 8192,
-    // 32/8 heads of 128, 640 (632, 985: keys of both sequences are more than the L2),
-    // 40 x 300 79 (73, 74).
+    // Runs of 8 of the last tiles, where sequences have two runs, not much fewer places
+    // hold them all and a launch is nowhere near its most: 6 x 1999 tokens, 16 heads
+    // of 64, 58 us (68 a sequence after the other, 57 in runs of 1), 4 x 8192 of them
+    // 501 (537, 590), 2 x 8192, 32/8 heads of 128, 640 (632, 985: keys of both
+    // sequences are more than the L2), 40 x 300 79 (73, 74).
     const int64_t even = ((int64_t)(max_new > 0 ? max_new : rows) * group + kTileRows - 1) / kTileRows;
     if (even == 1) {
         // a tile each: parts of one sequence after another, of which the last are short
@@ -57,7 +57,7 @@ Tiling tile_rows(const gemv_kv_cache* c, int64_t rows, int batch, int group, int
         t.order = kSingle;
         t.tiles = batch;
         t.run = 1;
-    } else if (even >= 16 && even * batch <= 2 * t.tiles) {
+    } else if (even >= 16 && even * batch <= 2 * t.tiles && even * batch * c->heads < 1 << 20) {
         t.order = kLaps;
         t.tiles = even;
         t.laps = batch;
