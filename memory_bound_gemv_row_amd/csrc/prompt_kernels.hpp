@@ -282,10 +282,13 @@ __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 // that the 16 rows that a read of keys takes at a time, and the four rows of
 // 64 bytes that a read of values does, are in different banks.
 //
-// Masks are looked at in tiles that some row of the workgroup does not see whole.
-// There the values may hold NaN or infinities in slots that only some rows
-// see; 0 * NaN would bring them to the others, so where there are any such a tile
-// is multiplied key by key, and rows that do not see the key keep their sums.
+// Masks are looked at in tiles that some row of the wave does not see whole, each
+// wave for itself, 32 keys at a time, and those that none of its rows sees left
+// out (8 x 4000 tokens through a window of 512: 294 us where a tile is whole or
+// masked for all waves, 272; 300 tokens 14.3 and 13.3).  There the values may
+// hold NaN or infinities in slots that only some rows see; 0 * NaN would bring
+// them to the others, so where there are any such a tile is multiplied key by
+// key, and rows that do not see the key keep their sums.
 template <int DP>
 struct PromptShared {
     u32x4 buffers[2][2][kTileKeys * DP / 8];                    // keys and values of a step, and of the next
@@ -582,16 +585,26 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
     auto use_masked = [&](const u32x4* keys, const u32x4* values, uint64_t held, int j0) {
 #pragma unroll 1
         for (int t = 0; t < 2; ++t, keys += 32 * CH, values += 32 * CH, held >>= 32, j0 += 32) {
+            // bit j: this lane's row sees slot j0 + j
+            auto look_at = [&] {
+                unsigned seen = bits_below((int64_t)position + 1 - j0);
+                if (a.window > 0)
+                    seen &= ~bits_below((int64_t)position + 1 - a.window - j0) | bits_below((int64_t)a.sinks - j0);
+                return seen & (unsigned)held;
+            };
+            unsigned visible = 0;
+            if constexpr (kOutputs == 1) {
+                visible = look_at();
+                if (!__any(visible != 0))
+                    continue;
+            }
             f32x16 s = f32x16{};
 #pragma unroll
             for (int e = 0; e < kSteps; ++e)
                 s = mfma_wide<DT>(keys[key_piece_at(0, e)], query[e], s);
-            // bit j: this lane's row sees slot j0 + j
-            unsigned seen = bits_below((int64_t)position + 1 - j0);
-            if (a.window > 0)
-                seen &= ~bits_below((int64_t)position + 1 - a.window - j0) | bits_below((int64_t)a.sinks - j0);
-            const unsigned visible = seen & (unsigned)held;
-            seen = visible >> (4 * half);   // element i is bit 8 (i / 4) + i % 4
+            if constexpr (kOutputs > 1)   // there registers are short: 332 us against 486 for 2 x 4096 tokens, 16/4 heads of 256
+                visible = look_at();
+            const unsigned seen = visible >> (4 * half);   // element i is bit 8 (i / 4) + i % 4
             float top = -kInf;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -605,15 +618,17 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
                 p[i / 8][i % 8 / 2] = power_pair(s[i], s[i + 1], ref);
             constexpr unsigned kExp = DT == kF16 ? 0x7C007C00u : 0x7F807F80u, kLow = DT == kF16 ? 0x04000400u : 0x00800080u;
             unsigned over = 0;
+            if (__any(there && visible != ~0u)) {
 #pragma unroll
-            for (int k = 0; k < kBlocks; ++k)
+                for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const u32x4 x = value(values, e, k);
+                    for (int e = 0; e < 2; ++e) {
+                        const u32x4 x = value(values, e, k);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        over |= (x[w] & kExp) + kLow;
-                }
+                        for (int w = 0; w < 4; ++w)
+                            over |= (x[w] & kExp) + kLow;
+                    }
+            }
             if (!__any((over & 0x80008000u) != 0)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
@@ -681,19 +696,18 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
                 fetch(which ^ 1, u + 1, next);
             next = look(u + 2);
         };
-        // every row of the workgroup sees all of step u
+        // this wave has rows, and each sees all of step u
         auto whole = [&] {
             const int j0 = slot_of(u);
-            return j0 + kTileKeys - 1 <= tile_min &&
-                   (a.window == 0 || j0 > tile_max - a.window || j0 + kTileKeys - 1 < a.sinks) &&
+            return mine && j0 + kTileKeys - 1 <= wave_min &&
+                   (a.window == 0 || j0 > wave_max - a.window || j0 + kTileKeys - 1 < a.sinks) &&
                    held_of(held_bits[which]) == ~0ull;
         };
         step();
         for (;;) {
             // most steps: a loop of its own, so that what the others need costs it no registers
             while (whole()) {
-                if (mine)
-                    use(buffers[which][0], buffers[which][1]);
+                use(buffers[which][0], buffers[which][1]);
                 if (++u >= end)
                     break;
                 which ^= 1;
