@@ -166,7 +166,9 @@ __device__ __forceinline__ int kind_at(const Rotate& a, int turn, int per, int* 
 // they are those at 8 u and rotated / 2 + 8 u, with neighbours as pairs those at
 // 16 u and 16 u + 8: a lane's pairs are its own, and both times its angles are
 // 8 u .. 8 u + 7.  Loose halves are held like neighbours, and each element's other
-// half comes over LDS.  A head takes 1 to 16 lanes, a step 64 / lanes heads of a
+// half comes over LDS, with angles by element (3001 tokens of 40 + 8 + 8 heads of 80, 70
+// rotated: 19 us; with angles by pair, chosen per element, 37, for that takes the
+// registers of two waves).  A head takes 1 to 16 lanes, a step 64 / lanes heads of a
 // kind.  The angles of a row are taken once, one a lane, and meet the heads over
 // LDS.
 //
@@ -178,8 +180,14 @@ rotate_kernel(Rotate a)
 {
     typedef typename Elem<IN>::wide In;
     typedef typename Elem<OUT>::wide Out;
-    __shared__ __attribute__((aligned(16))) float cosines[kWaves][kMaxDim / 2], sines[kWaves][kMaxDim / 2];
-    __shared__ __attribute__((aligned(16))) float others[PAIRING == kLoose ? kWaves : 1][PAIRING == kLoose ? 64 * 16 : 1];
+    // of loose halves, for each rotated element its pair's cosine and sine, with its own
+    // sign, and each step's elements; a lane's sixteen words are followed by one more,
+    // so that lanes meet in no bank
+    constexpr int kApart = 17;
+    constexpr int kAngles = PAIRING == kLoose ? kMaxDim / 16 * kApart : kMaxDim / 2;
+    __shared__ __attribute__((aligned(16))) float cosines[kWaves][kAngles], sines[kWaves][kAngles];
+    __shared__ float others[PAIRING == kLoose ? kWaves : 1][PAIRING == kLoose ? 64 * kApart : 1];
+    auto word = [](int d) { return d / 16 * kApart + d % 16; };
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int spans = (a.turns + a.span - 1) / a.span;
@@ -198,6 +206,16 @@ rotate_kernel(Rotate a)
         second = turned ? half + first : first + 8;
     }
     const bool both = live && second < a.dim;
+    int other[PAIRING == kLoose ? 16 : 1];   // where each element's other half lies among the lane's head's
+    unsigned rotates = 0;                    // bit per element
+    if constexpr (PAIRING == kLoose) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int d = first + e;
+            other[e] = word(d < half ? d + half : d < a.rotated ? d - half : d);
+            rotates |= (unsigned)(d < a.rotated) << e;
+        }
+    }
 
     f32x8 weight_first, weight_second;
     int weights_of = -1;
@@ -222,23 +240,26 @@ rotate_kernel(Rotate a)
         const int position = a.positions[row];
         for (int i = lane; i < half; i += 64) {
             const float2 t = turn_of(position, a.freqs[i]);
-            cosines[wave][i] = t.x;
-            sines[wave][i] = t.y;
+            if constexpr (PAIRING == kLoose) {
+                cosines[wave][word(i)] = cosines[wave][word(i + half)] = t.x;
+                sines[wave][word(i)] = -t.y;
+                sines[wave][word(i + half)] = t.y;
+            } else {
+                cosines[wave][i] = t.x;
+                sines[wave][i] = t.y;
+            }
         }
         // a wave reads what it wrote itself, and LDS takes its accesses in order
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         f32x8 c = {}, s = {}, c_second = {}, s_second = {};
-        int other[PAIRING == kLoose ? 16 : 1];   // where each element's other half lies among the lane's head's
         if constexpr (PAIRING == kLoose) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int d = first + e, pair = d < half ? d : d - half;
-                const bool is = d < a.rotated;
-                other[e] = !is ? d : d < half ? d + half : d - half;
-                const float cosine = is ? cosines[wave][pair] : 1.0f, sine = is ? sines[wave][pair] : 0.0f;
-                (e < 8 ? c : c_second)[e & 7] = cosine;
-                (e < 8 ? s : s_second)[e & 7] = d < half ? -sine : sine;
+            for (int e = 0; e < 8; ++e) {
+                c[e] = cosines[wave][unit * kApart + e];
+                s[e] = sines[wave][unit * kApart + e];
+                c_second[e] = cosines[wave][unit * kApart + 8 + e];
+                s_second[e] = sines[wave][unit * kApart + 8 + e];
             }
         } else if (live && turned) {
             c = *reinterpret_cast<const f32x8*>(&cosines[wave][8 * unit]);
@@ -293,16 +314,19 @@ rotate_kernel(Rotate a)
                         y = q * c + p * s;
                     }
                 } else {
-                    float* const mine_all = &others[wave][group * a.lanes * 16];
-                    *reinterpret_cast<f32x8*>(&mine_all[first]) = x;
-                    *reinterpret_cast<f32x8*>(&mine_all[second]) = y;
+                    float* const mine_all = &others[wave][group * a.lanes * kApart];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        mine_all[unit * kApart + e] = x[e];
+                        mine_all[unit * kApart + 8 + e] = y[e];
+                    }
                     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                     __builtin_amdgcn_wave_barrier();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float p = mine_all[other[e]], q = mine_all[other[8 + e]];
-                        x[e] = first + e < a.rotated ? x[e] * c[e] + p * s[e] : x[e];
-                        y[e] = second + e < a.rotated ? y[e] * c_second[e] + q * s_second[e] : y[e];
+                        x[e] = rotates >> e & 1 ? x[e] * c[e] + p * s[e] : x[e];
+                        y[e] = rotates >> (8 + e) & 1 ? y[e] * c_second[e] + q * s_second[e] : y[e];
                     }
                     __builtin_amdgcn_wave_barrier();   // the next step's writes come after these reads
                 }
