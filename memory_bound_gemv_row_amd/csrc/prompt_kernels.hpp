@@ -272,11 +272,12 @@ __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 // Bound, where prompts are long, by the matrix and the vector units in turn: both
 // are busy 45 % of the time and a SIMD's two waves only partly overlap, for all
 // wait for each tile of keys at one barrier (2 x 16384 tokens through a window of
-// 4096, 32/8 heads of 128: 1706 us, 959 TFLOP/s; the products and barriers alone
-// take 64 % of a long prompt's time, exponentials 10 %, reads of LDS 16 %, loads
-// 17 %, the maximum 3 %, each taken out by itself).  Where rows are few, by memory: 4 x
-// 7 tokens behind up to 65536 read 715 MB in 131 us.  Of a few hundred rows, by the
-// 1.1 to 2 us that a step takes however few waves there are.
+// 4096, 32/8 heads of 128: 1706 to 1780 us, 919 to 959 TFLOP/s; the products and
+// barriers alone take 64 % of a long prompt's time, exponentials 10 %, reads of
+// LDS 16 %, loads 17 %, the maximum 3 %, each taken out by itself).  Where rows
+// are few, by memory: 4 x 7 tokens behind up to 65536 read 715 MB in 131 us.  Of
+// a few hundred rows, by the 1.1 to 2 us that a step takes however few waves
+// there are.
 //
 // Places in LDS: piece c (16 bytes) of key row r lies at c ^ swizzle(r), such
 // that the 16 rows that a read of keys takes at a time, and the four rows of

@@ -162,15 +162,15 @@ __device__ __forceinline__ int kind_at(const Rotate& a, int turn, int per, int* 
 }
 
 // A wave per row (or per `span` of its steps where there are few rows).  A lane
-// holds two pieces of eight elements of a head.  With halves of whole pieces
-// they are those at 8 u and rotated / 2 + 8 u, with neighbours as pairs those at
-// 16 u and 16 u + 8: a lane's pairs are its own, and both times its angles are
-// 8 u .. 8 u + 7.  Loose halves are held like neighbours, and each element's other
-// half comes over LDS, with angles by element (3001 tokens of 40 + 8 + 8 heads of 80, 70
-// rotated: 19 us; with angles by pair, chosen per element, 37, for that takes the
-// registers of two waves).  A head takes 1 to 16 lanes, a step 64 / lanes heads of a
-// kind.  The angles of a row are taken once, one a lane, and meet the heads over
-// LDS.
+// holds two pieces of eight elements of a head.  With halves of whole pieces they
+// are those at 8 u and rotated / 2 + 8 u, with neighbours as pairs those at 16 u
+// and 16 u + 8: a lane's pairs are its own, and both times its angles are 8 u ..
+// 8 u + 7.  Loose halves are held like neighbours, and each element's other half
+// comes over LDS, with angles by element (3001 tokens of 40 + 8 + 8 heads of 80,
+// 70 rotated: 19 us; with angles by pair, chosen per element, 37, for that leaves
+// registers for two waves a SIMD).  A head takes 1 to 16 lanes, a step 64 / lanes
+// heads of a kind.  The angles of a row are taken once, one a lane, and meet the
+// heads over LDS.
 //
 // 8191 tokens of 32 + 8 + 8 heads of 128 (bfloat16) into a cache: 43.5 us, 4.6
 // TB/s read and written, where a copy makes 4.95; one token 3.7 us.
