@@ -177,9 +177,8 @@ const void* tiled_sized(Form form, int dim)
         if (dim == 256)
             return form_of<DT, 256, 16, true>(form);
     }
-    if (dim > 64 && dim <= 96)   // rows of 12 pieces: a load's are not of one run of 8
-        return form_of<DT, 96, RUN == 8 ? 1 : RUN, false>(form);
     return dim <= 64    ? form_of<DT, 64, RUN, false>(form)
+           : dim <= 96  ? form_of<DT, 96, RUN, false>(form)
            : dim <= 128 ? form_of<DT, 128, RUN, false>(form) : form_of<DT, 256, RUN, false>(form);
 }
 

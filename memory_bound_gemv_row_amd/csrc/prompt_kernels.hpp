@@ -430,15 +430,17 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
     unsigned piece[kKinds][kLoads];   // bytes from the row's start; of runs: from the run's first row's
     constexpr bool kRun = RUN > 1;
     constexpr int kRuns = kRun ? 16 / RUN : 1;
-    static_assert(RUN != 8 || 8 * CH % 64 == 0, "a load has rows of one run");
-    auto run_of = [](int i) { return kRun ? i * 64 / CH / RUN : 0; };   // of load i
+    // the run of a load's first piece, and the lane from which on its pieces are of the
+    // next one: none, but of heads of 96 in runs of eight the second load's middle
+    auto run_of = [](int i) { return kRun ? i * 64 / CH / RUN : 0; };
+    auto next_from = [run_of](int i) { return kRun ? (run_of(i) + 1) * RUN * CH - i * 64 : 64; };
 #pragma unroll
     for (int x = 0; x < kKinds; ++x)
         pool[x] = (x + output == 0 ? a.k : a.v) + kv * a.at.stride_head;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int p = i * 64 + lane, rw = p / CH, c = p - rw * CH;
-        load_row[i] = rw - run_of(i) * RUN;
+        load_row[i] = rw - (kRun ? run_of(i) * RUN + (lane < next_from(i) ? 0 : RUN) : 0);
 #pragma unroll
         for (int x = 0; x < kKinds; ++x) {
             const int at = c ^ (x + output == 0 ? key_swizzle(rw) : value_swizzle(rw));
@@ -494,8 +496,14 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
 #pragma unroll
-                for (int x = 0; x < kKinds; ++x)
-                    piece_to_lds(from[run_of(i)][x], load_row[i] < left[run_of(i)] ? piece[x][i] : kNowhere, to + x * kHalfBytes + i * 1024);
+                for (int x = 0; x < kKinds; ++x) {
+                    const unsigned at = to + x * kHalfBytes + i * 1024;
+                    const int run = run_of(i);
+                    if (lane < next_from(i))
+                        piece_to_lds(from[run][x], load_row[i] < left[run] ? piece[x][i] : kNowhere, at);
+                    else if (run + 1 < kRuns)
+                        piece_to_lds(from[run + 1][x], load_row[i] < left[run + 1] ? piece[x][i] : kNowhere, at);
+                }
         } else {
             bits = 0;
 #pragma unroll
