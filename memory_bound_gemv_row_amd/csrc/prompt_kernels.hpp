@@ -11,6 +11,8 @@
 
 #include "attention_kernels.hpp"
 
+#include <type_traits>
+
 namespace gattn {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -22,6 +24,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr int kTileRows = 128;   // query rows of a workgroup, 32 a wave
 constexpr int kTileKeys = 64;    // keys of a step, 16 loaded by each wave
 constexpr int kEverySlot = 0x7FFFFFFE;
+constexpr float kFar = 1 << 20;  // of scaled logits: half their step there, 2^-4, is little beside the slack
 
 // Waves that have the same 32 rows, and share out the output's elements: heads of
 // over 128 need two, for the sums of 256 elements leave no registers to work with.
@@ -546,7 +549,7 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
     };
     // the running maximum and all sums, where some logit passes it by kSlack
     auto raise = [&](float top) {
-        if (__any(top > m + a.slack)) {
+        if (__any(top - m > a.slack)) {
             top = fmaxf(top, __shfl_xor(top, 32));
             const float next = fmaxf(m, top);
             const float f = m == -kInf ? 0.0f : exp2_hw((m - next) * a.scale);
@@ -556,15 +559,26 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
             for (int k = 0; k < kBlocks; ++k)
                 acc[k] *= f;
         }
-        return m == -kInf ? 0.0f : m * a.scale;
+        return m == -kInf ? 0.0f : m;
     };
-    auto power_pair = [&](float x, float y, float ref) {
-        const unsigned pair = narrow_pair<DT>(exp2_hw(__builtin_fmaf(x, a.scale, -ref)), exp2_hw(__builtin_fmaf(y, a.scale, -ref)));
+    // Two powers.  A logit is subtracted from before it is scaled, so that the largest
+    // has power 1 and equal ones equal powers, however large they are.  Fused: in
+    // one operation, from a product that is rounded already; what that left off
+    // multiplies all powers of a row alike, up to 2^(half a step of the product).
+    constexpr bool kFused = kOutputs == 1;
+    auto power_pair = [&](auto fused, float x, float y, float from) {
+        auto power = [&](float z) {
+            return exp2_hw(decltype(fused)::value ? __builtin_fmaf(z, a.scale, -from) : (z - from) * a.scale);
+        };
+        const unsigned pair = narrow_pair<DT>(power(x), power(y));
         sum = add_pair<DT>(pair, sum);
         return pair;
     };
 
-    // a tile that every row sees whole
+    // A tile that every row sees whole; or false, and nothing summed, where powers are
+    // fused and some logits are too far from zero for that.  (Not fused at all: 4 x 8192
+    // tokens, 16 heads of 64, 520 us for 494, 2 x 8192, 32/8 of 128, 642 for 629.  Heads of
+    // over 128 have no registers for the other way out: 329 us to 489 by it, 332 without.)
     auto use = [&](const u32x4* keys, const u32x4* values) {
         f32x16 s[2];
 #pragma unroll
@@ -578,16 +592,22 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
 #pragma unroll
         for (int i = 1; i < 32; ++i)
             top = fmaxf(top, s[i / 16][i % 16]);
-        const float ref = raise(top);
+        float from = raise(top);
+        if constexpr (kFused) {
+            from *= a.scale;
+            if (__any(fabsf(from) > kFar))
+                return false;
+        }
         u32x4 p[4];
 #pragma unroll
         for (int i = 0; i < 32; i += 2)
-            p[i / 8][i % 8 / 2] = power_pair(s[i / 16][i % 16], s[i / 16][i % 16 + 1], ref);
+            p[i / 8][i % 8 / 2] = power_pair(std::bool_constant<kFused>{}, s[i / 16][i % 16], s[i / 16][i % 16 + 1], from);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int k = 0; k < kBlocks; ++k)
                 acc[k] = mfma_wide<DT>(value(values, e, k), p[e], acc[k]);
+        return true;
     };
 
     // any other tile, 32 keys at a time
@@ -620,11 +640,11 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
                 s[i] = seen >> (8 * (i / 4) + i % 4) & 1 ? s[i] : -kInf;
                 top = fmaxf(top, s[i]);
             }
-            const float ref = raise(top);
+            const float from = raise(top);
             u32x4 p[2];
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
-                p[i / 8][i % 8 / 2] = power_pair(s[i], s[i + 1], ref);
+                p[i / 8][i % 8 / 2] = power_pair(std::false_type{}, s[i], s[i + 1], from);
             constexpr unsigned kExp = DT == kF16 ? 0x7C007C00u : 0x7F807F80u, kLow = DT == kF16 ? 0x04000400u : 0x00800080u;
             unsigned over = 0;
             if (__any(there && visible != ~0u)) {
@@ -715,8 +735,7 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
         step();
         for (;;) {
             // most steps: a loop of its own, so that what the others need costs it no registers
-            while (whole()) {
-                use(buffers[which][0], buffers[which][1]);
+            while (whole() && use(buffers[which][0], buffers[which][1])) {
                 if (++u >= end)
                     break;
                 which ^= 1;
