@@ -24,6 +24,13 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr int kTileRows = 128;   // query rows of a workgroup, 32 a wave
 constexpr int kTileKeys = 64;    // keys of a step, 16 loaded by each wave
 constexpr int kEverySlot = 0x7FFFFFFE;
+
+// The power of two that a row's largest power has where its logit is the running
+// maximum.  binary16 has room for 2^15, of which the slack takes eight, and loses
+// what is below 2^-14 bit by bit: so raised, a power is rounded by half a step down
+// to 2^-21 of the largest, and by 2^-32 of the largest below that.
+constexpr float raised_of(int type) { return type == kF16 ? 7.0f : 0.0f; }
+constexpr float lowered_of(int type) { return type == kF16 ? 0x1p-7f : 1.0f; }
 constexpr float kFar = 1 << 20;  // of scaled logits: half their step there, 2^-4, is little beside the slack
 
 // Waves that have the same 32 rows, and share out the output's elements: heads of
@@ -263,9 +270,9 @@ __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 // The powers, in pairs rounded to 16 bits, are in place as the right operand of
 // the product with the values, if that takes its summed index in the same
 // order of keys; the left operand, columns of four values, comes out of LDS
-// turned by ds_read_b64_tr_b16.  The powers' rounding, half a step of 2^-11 or
-// 2^-8 relative each, is below that of the output, which averages over them;
-// the sum is taken over the rounded powers, so the weights still add up to one.
+// turned by ds_read_b64_tr_b16.  The powers' rounding is half a step, 2^-11 or 2^-8
+// relative each (see raised_of); the sum is taken over the rounded powers, so the
+// weights still add up to one.
 //
 // RUN: slots that lie in one page from their first multiple on, 16 or 8, whose
 // address is the same for all lanes; 1: each row has an address of its own (4 x
@@ -561,14 +568,15 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
         }
         return m == -kInf ? 0.0f : m;
     };
-    // Two powers.  A logit is subtracted from before it is scaled, so that the largest
-    // has power 1 and equal ones equal powers, however large they are.  Fused: in
-    // one operation, from a product that is rounded already; what that left off
-    // multiplies all powers of a row alike, up to 2^(half a step of the product).
+    // Two powers, times 2^raised.  A logit is subtracted from before it is scaled, so
+    // that the largest has power 1 and equal ones equal powers, however large they
+    // are.  Fused: in one operation, from a product that is rounded already; what that
+    // left off multiplies all powers of a row alike, up to 2^(half a step of the product).
     constexpr bool kFused = kOutputs == 1;
+    constexpr float kRaised = raised_of(DT), kLowered = lowered_of(DT);
     auto power_pair = [&](auto fused, float x, float y, float from) {
         auto power = [&](float z) {
-            return exp2_hw(decltype(fused)::value ? __builtin_fmaf(z, a.scale, -from) : (z - from) * a.scale);
+            return exp2_hw(decltype(fused)::value ? __builtin_fmaf(z, a.scale, -from) : __builtin_fmaf(z - from, a.scale, kRaised));
         };
         const unsigned pair = narrow_pair<DT>(power(x), power(y));
         sum = add_pair<DT>(pair, sum);
@@ -594,7 +602,7 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
             top = fmaxf(top, s[i / 16][i % 16]);
         float from = raise(top);
         if constexpr (kFused) {
-            from *= a.scale;
+            from = __builtin_fmaf(from, a.scale, -kRaised);
             if (__any(fabsf(from) > kFar))
                 return false;
         }
@@ -762,7 +770,7 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
         const int64_t to_part = at * a.parts + part;
         if (half == 0 && output == 0) {
             a.part_ms[to_part * 2] = m == -kInf ? -kInf : m * a.scale;
-            a.part_ms[to_part * 2 + 1] = sum;
+            a.part_ms[to_part * 2 + 1] = sum * kLowered;
             // parts that this sequence does not have saw nothing
             if (a.order == kShares)
                 for (int p = parts + part; p < a.parts; p += parts) {
@@ -778,7 +786,7 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
                     const int d = 32 * (kBlocks * output + k) + 8 * i + 4 * half;
                     if (EXACT || d < a.dim)
                         *reinterpret_cast<f32x4*>(a.part_out + to_part * a.dim + d) =
-                            f32x4{acc[k][4 * i], acc[k][4 * i + 1], acc[k][4 * i + 2], acc[k][4 * i + 3]};
+                            f32x4{acc[k][4 * i], acc[k][4 * i + 1], acc[k][4 * i + 2], acc[k][4 * i + 3]} * kLowered;
                 }
         return;
     }
