@@ -45,7 +45,8 @@ extern "C" {
  * above -inf) gets zeros; what a row does not see does not touch it, NaN and
  * infinities included.  Sums and the softmax are kept in binary32; where max_new
  * is above 1 the powers are rounded to the cache's type before they meet the
- * values.
+ * values: by half a step, or in binary16, where that is more, by 2^-32 of the row's
+ * largest power.
  * GEMV_E_INVAL for negative sizes, a missing pointer (starts too, where max_new
  * is not 1 or rows < batch), window < 0 or sinks < 0, or too small a workspace;
  * GEMV_E_UNSUPPORTED as for gemv_attention, for out not 16-byte aligned,
@@ -71,7 +72,7 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
  *   batch, q, out, zeros, special values and statuses as for gemv_attention
  *   (without weights); out 16-byte aligned.
  * The two may share pages.  The powers of the prefix are rounded to the
- * cache's type before they meet its values, others are not. */
+ * cache's type before they meet its values, as above; others are not. */
 size_t gemv_prefix_attention_workspace(const gemv_kv_cache* cache, const gemv_kv_batch* prefixes,
                                        const gemv_kv_batch* batch, int q_heads);
 
