@@ -48,7 +48,8 @@ extern "C" {
  * values: by half a step, or in binary16, where that is more, by 2^-32 of the row's
  * largest power.
  * GEMV_E_INVAL for negative sizes, a missing pointer (starts too, where max_new
- * is not 1 or rows < batch), window < 0 or sinks < 0, or too small a workspace;
+ * is not 1 or rows < batch), window < 0 or sinks < 0, an out that shares memory with
+ * q's rows otherwise than as said, or too small a workspace;
  * GEMV_E_UNSUPPORTED as for gemv_attention, for out not 16-byte aligned,
  * for more than 2^30 rows of heads, and where a launch would pass 2^30 work-items
  * (about 4 million tiles of 128 query rows, or joins of 4). */

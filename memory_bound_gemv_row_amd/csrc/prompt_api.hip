@@ -345,6 +345,20 @@ int check_query(const void* q, int64_t q_stride, const void* out)
     return q_stride % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) ? GEMV_E_UNSUPPORTED : GEMV_OK;
 }
 
+// Whether out's dense rows of `width` elements are q's own, or share no memory with them:
+// otherwise rows are written that other workgroups have yet to read.
+bool in_place_or_apart(const void* q, int64_t q_stride, const void* out, int64_t rows, int64_t width)
+{
+    const uintptr_t from = reinterpret_cast<uintptr_t>(q), to = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t row = (uintptr_t)width * 2, step = (uintptr_t)q_stride * 2, bytes = (uintptr_t)rows * row;
+    if (to == from)
+        return q_stride == width || rows == 1;
+    if (to < from)
+        return from - to >= bytes;
+    const uintptr_t i = (to - from) / step, into = (to - from) % step;   // the last row of q that begins at or before out
+    return i >= (uintptr_t)rows || (into >= row && (i + 1 == (uintptr_t)rows || step - into >= bytes));
+}
+
 // Rows, and sequences of heads, that no launch has work-items for, whose products
 // with what follows could pass 64 bits.
 bool countable(int64_t rows, int64_t q_heads, int64_t batch, int64_t heads)
@@ -395,6 +409,8 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
         return rc;
     if (!countable(rows, q_heads, batch->batch, cache->heads))
         return GEMV_E_UNSUPPORTED;
+    if (!in_place_or_apart(q, q_stride, out, starts != nullptr ? rows : batch->batch, (int64_t)q_heads * cache->head_dim))
+        return GEMV_E_INVAL;
     gemv_device::Device dev{};
     if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
         return rc;
@@ -484,6 +500,8 @@ int gemv_prefix_attention(const gemv_kv_cache* cache, const gemv_kv_batch* prefi
         return rc;
     if (!countable(batch->batch, q_heads, (int64_t)batch->batch + prefixes->batch, cache->heads))
         return GEMV_E_UNSUPPORTED;
+    if (!in_place_or_apart(q, q_stride, out, batch->batch, (int64_t)q_heads * cache->head_dim))
+        return GEMV_E_INVAL;
     gemv_device::Device dev{};
     if (int rc = gemv_device::current(&dev); rc != GEMV_OK)
         return rc;
