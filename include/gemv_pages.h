@@ -52,8 +52,9 @@ typedef struct gemv_page_pool {
  * written: what lies from count_out[0] to count[0] has been taken.  The outputs overlap
  * neither each other nor the inputs.  Lengths are taken as 0 to 2^31 - 1 with
  * what is added.
- * GEMV_E_INVAL for negative sizes, page_size below 1, table_stride below width or
- * a missing pointer; GEMV_E_UNSUPPORTED for more than 2^30 rows. */
+ * GEMV_E_INVAL for negative sizes, page_size below 1, table_stride below width, a
+ * missing pointer or outputs that overlap (of a table whose rows lie apart, its first
+ * row is looked at); GEMV_E_UNSUPPORTED for more than 2^30 rows. */
 int gemv_reserve_pages(const gemv_page_pool* pool, const int32_t* lens, const int32_t* added, int rows,
                        int32_t* count_out, int32_t* lens_out, int32_t* starts, int32_t* positions, int64_t* slots,
                        hipStream_t stream);
@@ -64,7 +65,7 @@ int gemv_reserve_pages(const gemv_page_pool* pool, const int32_t* lens, const in
  * are put on the stack in the order of sequences and entries, and the entries
  * become -1.  Entries that name no page are not put there, nor pages past the
  * stack's room: a page given back must stand in one table, once.
- *   count_out  int32 [2]: free pages now, and 0; not count itself;
+ *   count_out  int32 [2]: free pages now, and 0; it overlaps no input;
  *   workspace  of at least gemv_release_pages_workspace bytes, 16-byte aligned,
  *              one for each call that may run at once.
  * GEMV_E_INVAL as above, and for too small a workspace; GEMV_E_UNSUPPORTED for

@@ -992,6 +992,12 @@ def _pool(free, count, table, page_size, here):
     return Pool(fp, cp, pages, page_size, tp, stride, width, B)
 
 
+def _held(pool):
+    """(address, bytes) of the stack and of the table."""
+    span = (pool.batch - 1) * pool.table_stride + pool.width if pool.batch else 0
+    return [(pool.free_pages or 0, 4 * pool.pages), (pool.table or 0, 4 * span)]
+
+
 def reserve_pages(free, count, table, lens, added, page_size, rows, out=None, stream=None):
     """Room for added[b] new tokens of each sequence b, of lens[b] so far (int32
     [batch]): pages from the stack free[: count[0]] (free int32 [pages of the
@@ -1023,8 +1029,7 @@ def reserve_pages(free, count, table, lens, added, page_size, rows, out=None, st
     else:
         outs = [_ptr(t, f"out[{i}]", dtype, (n,), here) for i, (t, (_, dtype, n)) in enumerate(zip(out, shapes, strict=True))]
         size = [n * (8 if dtype is torch.int64 else 4) for _, dtype, n in shapes]
-        _apart(list(zip(outs, size)), [(lp, 4 * B), (ap, 4 * B), (pool.count, 8), (pool.free_pages, 4 * pool.pages),
-                                       (pool.table, 4 * ((B - 1) * pool.table_stride + pool.width) if B else 0)])
+        _apart(list(zip(outs, size)), [(lp, 4 * B), (ap, 4 * B), (pool.count, 8)] + _held(pool))
     _check(load().gemv_reserve_pages(ctypes.byref(pool), lp, ap, rows, *outs, handle), "gemv_reserve_pages")
     return out
 
@@ -1045,7 +1050,7 @@ def release_pages(free, count, table, keep, page_size, out=None, stream=None):
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", torch.int32, (2,), here)
-        _apart([(op, 8)], [(pool.count, 8), (kp, 4 * pool.batch)])
+        _apart([(op, 8)], [(pool.count, 8), (kp, 4 * pool.batch)] + _held(pool))
     lib, c = load(), ctypes.byref(pool)
     need = lib.gemv_release_pages_workspace(c)
     work = empty(need, dtype=torch.uint8, device=free.device) if need else None

@@ -5,6 +5,8 @@
 #include "attention_host.hpp"
 #include "pages_kernels.hpp"
 
+#include <initializer_list>
+
 namespace gpages {
 namespace {
 
@@ -23,6 +25,37 @@ int check(const gemv_page_pool* c, Pool* out)
     *out = Pool{c->free_pages, c->count, c->pages, c->page_size, gattn::divider(c->page_size), c->table, c->table_stride,
                 c->width, c->batch};
     return GEMV_OK;
+}
+
+struct Span {
+    const void* at;
+    int64_t bytes;
+};
+
+// That outputs share no memory with each other or with inputs, which other
+// workgroups still read while the first one writes.
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    auto meet = [](const Span& a, const Span& b) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
+        return a.bytes > 0 && b.bytes > 0 && p < q + (uintptr_t)b.bytes && q < p + (uintptr_t)a.bytes;
+    };
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span* other = o + 1; other != outs.end(); ++other)
+            if (meet(*o, *other))
+                return false;
+        for (const Span& in : ins)
+            if (meet(*o, in))
+                return false;
+    }
+    return true;
+}
+
+// the entries of a table whose rows follow each other; of another, its first row's
+Span entries(const gemv_page_pool* c)
+{
+    const int64_t rows = c->batch == 0 ? 0 : c->table_stride == c->width ? c->batch : 1;
+    return Span{c->table, rows * c->width * (int64_t)sizeof(int32_t)};
 }
 
 }  // namespace
@@ -44,6 +77,10 @@ int gemv_reserve_pages(const gemv_page_pool* pool, const int32_t* lens, const in
         return GEMV_E_INVAL;
     if (rows > (int)kMost)
         return GEMV_E_UNSUPPORTED;
+    const int64_t each = (int64_t)pool->batch * (int64_t)sizeof(int32_t);
+    if (!apart({{count_out, 8}, {lens_out, each}, {starts, each + 4}, {positions, 4 * (int64_t)rows}, {slots, 8 * (int64_t)rows}},
+               {{pool->count, 4}, {pool->free_pages, 4 * (int64_t)pool->pages}, entries(pool), {lens, each}, {added, each}}))
+        return GEMV_E_INVAL;
     a.lens = lens;
     a.added = added;
     a.rows = rows;
@@ -77,6 +114,10 @@ int gemv_release_pages(const gemv_page_pool* pool, const int32_t* keep, int32_t*
         return GEMV_E_UNSUPPORTED;
     const size_t need = gemv_release_pages_workspace(pool);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
+        return GEMV_E_INVAL;
+    if (!apart({{count_out, 8}, {workspace, (int64_t)need}},
+               {{pool->count, 4}, {pool->free_pages, 4 * (int64_t)pool->pages}, entries(pool),
+                {keep, (int64_t)pool->batch * (int64_t)sizeof(int32_t)}}))
         return GEMV_E_INVAL;
     a.keep = keep;
     a.count_out = count_out;
