@@ -56,8 +56,9 @@ typedef struct gemv_heads {
  * The bandwidth path needs 16-byte-aligned x, out and weights, and strides and
  * head_dim that are multiples of 8; others go element by element.
  * GEMV_E_INVAL for negative sizes, a stride below heads * head_dim, rotated odd
- * or outside [0, head_dim], an unknown type, a missing pointer, or an out that is
- * x in another type or stride;
+ * or outside [0, head_dim], an unknown type, a missing pointer, or an out whose
+ * rows share memory with x's in another type or stride, with the other's or with
+ * the other out's;
  * GEMV_E_UNSUPPORTED for head_dim over 256. */
 int gemv_norm_rotate(const gemv_rotation* how, const gemv_heads* q, const gemv_heads* k, int dtype, int out_dtype,
                      const int32_t* positions, int rows, hipStream_t stream);

@@ -30,11 +30,69 @@ int check_heads(const gemv_heads* h, int dim, int rows, bool own_out)
     return GEMV_OK;
 }
 
-// In place, or not at all: results laid over their inputs in another way would
-// meet elements that are still to be read.
-bool laid_alike(const gemv_heads* h, int in, int out)
+int bytes_of(int type) { return type == GEMV_F32 ? 4 : 2; }
+
+// Rows of `width` bytes, `step` apart.
+struct Rows {
+    uintptr_t at, width, step;
+};
+
+Rows inputs_of(const gemv_heads* h, int dim, int type)
 {
-    return h->out != h->x || h->out == nullptr || (in == out && h->stride == h->out_stride);
+    const uintptr_t size = bytes_of(type);
+    return Rows{reinterpret_cast<uintptr_t>(h->x), (uintptr_t)h->heads * dim * size, (uintptr_t)h->stride * size};
+}
+
+Rows outputs_of(const gemv_heads* h, int dim, int type)
+{
+    const uintptr_t size = bytes_of(type);
+    return Rows{reinterpret_cast<uintptr_t>(h->out), (uintptr_t)h->heads * dim * size, (uintptr_t)h->out_stride * size};
+}
+
+// Whether some row of one shares a byte with some row of the other; parts of a
+// product's rows, whose rows take turns, do not.
+bool meet(Rows a, Rows b, int rows)
+{
+    if (a.width == 0 || b.width == 0)
+        return false;
+    if (b.at < a.at) {
+        const Rows c = a;
+        a = b;
+        b = c;
+    }
+    const uintptr_t n = (uintptr_t)rows;
+    if (b.at >= a.at + (n - 1) * a.step + a.width)
+        return false;
+    if (a.step == b.step) {
+        const uintptr_t turns = (b.at - a.at) / a.step, into = (b.at - a.at) % a.step;   // a step is a row at least
+        return (turns < n && into < a.width) || (turns + 1 < n && a.step - into < b.width);
+    }
+    for (uintptr_t j = 0; j < n; ++j) {
+        const uintptr_t from = b.at + j * b.step, i = (from - a.at) / a.step, into = (from - a.at) % a.step;
+        if (i >= n)
+            break;
+        if (into < a.width || (i + 1 < n && a.step - into < b.width))
+            return true;
+    }
+    return false;
+}
+
+// Results in the place of their own inputs, or apart from all inputs and each other:
+// laid over them in another way they would meet elements that are still to be read.
+bool placed(const gemv_heads* const* of, int n, int outs, int dim, int in, int out, int rows)
+{
+    for (int i = 0; i < outs; ++i) {
+        const Rows o = outputs_of(of[i], dim, out);
+        for (int j = 0; j < n; ++j) {
+            const Rows x = inputs_of(of[j], dim, in);
+            const bool own = i == j && o.at == x.at && in == out && (o.step == x.step || rows == 1);
+            if (!own && meet(o, x, rows))
+                return false;
+            if (j < outs && j != i && meet(o, outputs_of(of[j], dim, out), rows))
+                return false;
+        }
+    }
+    return true;
 }
 
 // 16 bytes of every row, head and piece
@@ -143,9 +201,11 @@ int gemv_norm_rotate(const gemv_rotation* how, const gemv_heads* q, const gemv_h
     }
     if (rows == 0)
         return GEMV_OK;
-    if (!laid_alike(q, dtype, out_dtype) || (k != nullptr && !laid_alike(k, dtype, out_dtype)))
-        return GEMV_E_INVAL;
     if (positions == nullptr || (how->rotated > 0 && how->freqs == nullptr))
+        return GEMV_E_INVAL;
+    const gemv_heads* const both[2] = {q, k};
+    const int given = k != nullptr ? 2 : 1;
+    if (!placed(both, given, given, how->head_dim, dtype, out_dtype, rows))
         return GEMV_E_INVAL;
     Rotate a = rotation_of(how, positions, rows);
     a.of[kQuery] = heads_of(q, a.norm);
@@ -175,7 +235,8 @@ int gemv_norm_rotate_append(const gemv_rotation* how, const gemv_heads* q, const
         return GEMV_E_UNSUPPORTED;
     if (rows == 0)
         return GEMV_OK;
-    if (!laid_alike(q, dtype, cache->dtype))
+    const gemv_heads* const all[3] = {q, k, v};
+    if (!placed(all, 3, 1, how->head_dim, dtype, cache->dtype, rows))
         return GEMV_E_INVAL;
     if (positions == nullptr || slots == nullptr || (how->rotated > 0 && how->freqs == nullptr) ||
         (cache->pages > 0 && (cache->k == nullptr || cache->v == nullptr)))
