@@ -122,14 +122,14 @@ __device__ __forceinline__ void piece_to_lds([[maybe_unused]] u32x4 from, [[mayb
 {
 #ifdef __HIP_DEVICE_COMPILE__
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(to), "v"(offset), "s"(from) : "m0", "memory");
+                 :: "s"(to), "v"(offset), "s"(from) : "memory");
 #endif
 }
 
 __device__ __forceinline__ void piece_to_lds([[maybe_unused]] const void* from, [[maybe_unused]] unsigned to)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(to), "v"(from) : "m0", "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(to), "v"(from) : "memory");
 #endif
 }
 
