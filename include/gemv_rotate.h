@@ -59,7 +59,7 @@ typedef struct gemv_heads {
  * or outside [0, head_dim], an unknown type, a missing pointer, or an out whose
  * rows share memory with x's in another type or stride, with the other's or with
  * the other out's;
- * GEMV_E_UNSUPPORTED for head_dim over 256. */
+ * GEMV_E_UNSUPPORTED for head_dim over 256 and for more than 2^30 heads of a row. */
 int gemv_norm_rotate(const gemv_rotation* how, const gemv_heads* q, const gemv_heads* k, int dtype, int out_dtype,
                      const int32_t* positions, int rows, hipStream_t stream);
 

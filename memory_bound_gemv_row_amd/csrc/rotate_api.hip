@@ -102,6 +102,15 @@ bool wide(const gemv_heads* h, bool own_out)
            (!own_out || (aligned(h->out, 16) && h->out_stride % 8 == 0));
 }
 
+// a row's steps are counted in int, and no head is smaller than a step
+bool countable(const gemv_heads* const* of, int n)
+{
+    int64_t heads = 0;
+    for (int i = 0; i < n; ++i)
+        heads += of[i]->heads;
+    return heads <= gemv_device::kMaxWorkItems;
+}
+
 constexpr int kElements = -1;   // in the place of a pairing: element by element
 
 template <int IN, int OUT>
@@ -207,6 +216,8 @@ int gemv_norm_rotate(const gemv_rotation* how, const gemv_heads* q, const gemv_h
     const int given = k != nullptr ? 2 : 1;
     if (!placed(both, given, given, how->head_dim, dtype, out_dtype, rows))
         return GEMV_E_INVAL;
+    if (!countable(both, given))
+        return GEMV_E_UNSUPPORTED;
     Rotate a = rotation_of(how, positions, rows);
     a.of[kQuery] = heads_of(q, a.norm);
     if (k != nullptr)
@@ -238,6 +249,8 @@ int gemv_norm_rotate_append(const gemv_rotation* how, const gemv_heads* q, const
     const gemv_heads* const all[3] = {q, k, v};
     if (!placed(all, 3, 1, how->head_dim, dtype, cache->dtype, rows))
         return GEMV_E_INVAL;
+    if (!countable(all, 3))
+        return GEMV_E_UNSUPPORTED;
     if (positions == nullptr || slots == nullptr || (how->rotated > 0 && how->freqs == nullptr) ||
         (cache->pages > 0 && (cache->k == nullptr || cache->v == nullptr)))
         return GEMV_E_INVAL;

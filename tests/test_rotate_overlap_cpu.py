@@ -81,3 +81,10 @@ def test_against_sets_of_bytes(lib):   # noqa: F811
                     got = lib.gemv_norm_rotate(ctypes.byref(_how(head_dim=8, rotated=8, norm=0)), ctypes.byref(q), None, 0, 1, P - (1 << 19),
                                                rows, None)
                     assert (got == INVAL) == bool(meets), (heads, stride, out_stride, shift)
+
+
+def test_more_heads_than_are_counted(lib):   # noqa: F811
+    most, wide = (1 << 31) - 1, 64 << 31
+    q, k, v = (_heads(n, x=P, stride=wide, out=P + (at << 50), out_stride=wide) for n, at in ((most, 1), (most, 2), (2, 0)))
+    assert _turn(lib, q, k, 1) == 2 and _turn(lib, q, _heads(0), 1) == 2 and _turn(lib, _heads(0), k, 1) == 2
+    assert _put(lib, q, v, v, 1) == 2
