@@ -5,6 +5,8 @@
 #include "device_info.hpp"
 #include "rotate_kernels.hpp"
 
+#include <numeric>
+
 namespace grot {
 namespace {
 
@@ -67,7 +69,8 @@ bool meet(Rows a, Rows b, int rows)
         const uintptr_t turns = (b.at - a.at) / a.step, into = (b.at - a.at) % a.step;   // a step is a row at least
         return (turns < n && into < a.width) || (turns + 1 < n && a.step - into < b.width);
     }
-    for (uintptr_t j = 0; j < n; ++j) {
+    const uintptr_t period = a.step / std::gcd(a.step, b.step);   // rows of b until they lie to a's as before
+    for (uintptr_t j = 0; j < n && j < period; ++j) {
         const uintptr_t from = b.at + j * b.step, i = (from - a.at) / a.step, into = (from - a.at) % a.step;
         if (i >= n)
             break;
