@@ -252,6 +252,42 @@ __device__ __forceinline__ Share share_at(const Prompt& a, int w)
                  w - __builtin_amdgcn_readlane(upto, it) + own, own, chunk};
 }
 
+// The key-value head, the part of the keys, and the place among the head's row tiles
+// (of sequence `lap`, where a.order is kLaps) of a workgroup, for all orders but
+// kShares.
+//
+// Workgroups go to the eight XCDs in turn.  Those that read the same keys
+// (a head's, of a part) are on one XCD where such sets are a multiple of
+// eight, and the last parts, which only long sequences have, come first.  From
+// part to part an XCD moves on by a head, so that it sees every head's part of
+// the address space.  Of the row tiles the last, which see most, come first, a run
+// of them from one sequence before the next one's, so that they find its keys
+// in the L2, and all sequences' and sets' last run before the one before it, so that
+// what is started last is short.
+//
+// `quotient` divides two numbers that are the same for all lanes.
+struct Spot {
+    int kv, part, place, lap;
+};
+
+template <class Quotient>
+__host__ __device__ __forceinline__ Spot spot_of(const Prompt& a, int block, Quotient quotient)
+{
+    const int sets = a.heads * a.parts;
+    const bool eight = sets % 8 == 0;
+    const int each = eight ? sets >> 3 : 1;                                 // sets of an XCD
+    int j = eight ? block >> 3 : quotient(block, sets);
+    const int first = quotient(j, each * a.stretch);
+    j -= first * each * a.stretch;
+    const int left = a.tiles - first * a.run;
+    const int run = left < a.run ? left : a.run;
+    const int lap = quotient(j, run), set_of = quotient(lap, a.laps);
+    const int set = eight ? set_of * 8 + (block & 7) : block - quotient(block, sets) * sets;
+    const int part_back = quotient(set, a.heads), part = a.parts - 1 - part_back;
+    const int kv_at = set - part_back * a.heads + part;
+    return Spot{kv_at - quotient(kv_at, a.heads) * a.heads, part, a.tiles - 1 - first * a.run - (j - lap * run), lap - set_of * a.laps};
+}
+
 // 16 zeros that slots without a page are read from
 __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 
@@ -328,15 +364,6 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
     const int output = kOutputs == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
     const int half = lane >> 5;
 
-    // Workgroups go to the eight XCDs in turn.  Those that read the same keys
-    // (a head's, of a part) are on one XCD where such sets are a multiple of
-    // eight, and the last parts, which only long sequences have, come first.  From
-    // part to part an XCD moves on by a head, so that it sees every head's part of
-    // the address space.  Of the row tiles the last, which see most, come first, a run
-    // of them from one sequence before the next one's, so that they find its keys
-    // in the L2, and all sequences' and sets' last run before the one before it, so
-    // that what is started last is short.
-    const int sets = a.heads * a.parts;
     // `one`: the same for all lanes, and known to be where the vector unit has computed it
     auto one = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
     auto quotient = [&](int x, int y) { return one((int)((unsigned)x / (unsigned)y)); };
@@ -355,28 +382,17 @@ __device__ __forceinline__ void prompt_block(const Prompt& a, int block, PromptS
         const int kv_at = block - w * a.heads + part;
         kv = kv_at - quotient(kv_at, a.heads) * a.heads;
     } else {
-        const bool eight = sets % 8 == 0;
-        const int each = eight ? sets >> 3 : 1;                                 // sets of an XCD
-        int j = eight ? block >> 3 : quotient(block, sets);
-        const int first = quotient(j, each * a.stretch);
-        j -= first * each * a.stretch;
-        const int left = a.tiles - first * a.run;
-        const int run = left < a.run ? left : a.run;
-        const int lap = quotient(j, run), set_of = quotient(lap, a.laps);
-        const int set = eight ? set_of * 8 + (block & 7) : block - quotient(block, sets) * sets;
-        const int place = a.tiles - 1 - first * a.run - (j - lap * run);
-        const int part_back = quotient(set, a.heads);
-        part = a.parts - 1 - part_back;
-        const int kv_at = set - part_back * a.heads + part;
-        kv = kv_at - quotient(kv_at, a.heads) * a.heads;
-        tile = place;
+        const Spot spot = spot_of(a, block, quotient);
+        part = spot.part;
+        kv = spot.kv;
+        tile = spot.place;
         if (a.order != kTogether) {
-            const int at = a.order == kSingle ? place : lap - set_of * a.laps;
-            tile = a.order == kSingle ? 0 : place;
+            const int at = a.order == kSingle ? spot.place : spot.lap;
+            tile = a.order == kSingle ? 0 : spot.place;
             sequence = Sequence{at, a.at.length(at), (int)row_start(a.starts, at, a.rows), (int)row_start(a.starts, at + 1, a.rows)};
         } else {
-            sequence = sequence_at(a.at, a.starts, a.batch, a.rows, a.group, place);
-            tile = place - (int)((int64_t)sequence.from * a.group / kTileRows) - sequence.b;
+            sequence = sequence_at(a.at, a.starts, a.batch, a.rows, a.group, spot.place);
+            tile = spot.place - (int)((int64_t)sequence.from * a.group / kTileRows) - sequence.b;
         }
     }
     kv = one(kv);
