@@ -134,28 +134,28 @@ inline Split split_for(const gemv_kv_cache* c, const gemv_kv_batch* s, int limit
     return p;
 }
 
-template <int DT, bool WHOLE, int WAVES>
+template <int DT, bool WHOLE, int WAVES, bool VIEW>
 const void* attention_sized(int dim)
 {
     if constexpr (WHOLE) {
         if (dim == 64)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 64, true, true, WAVES>);
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 64, true, true, WAVES, VIEW>);
         if (dim == 128)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 128, true, true, WAVES>);
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 128, true, true, WAVES, VIEW>);
         if (dim == 256)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 256, true, true, WAVES>);
+            return reinterpret_cast<const void*>(&attention_kernel<DT, 256, true, true, WAVES, VIEW>);
     }
-    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64, WHOLE, false, WAVES>)
-           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128, WHOLE, false, WAVES>)
-                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256, WHOLE, false, WAVES>);
+    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64, WHOLE, false, WAVES, VIEW>)
+           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128, WHOLE, false, WAVES, VIEW>)
+                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256, WHOLE, false, WAVES, VIEW>);
 }
 
-template <int DT>
+template <int DT, bool VIEW = false>
 const void* attention_for(const gemv_kv_cache* c, bool lone)
 {
-    return lone             ? attention_sized<DT, true, kLoneWaves>(c->head_dim)
-           : whole_tiles(c) ? attention_sized<DT, true, kWaves>(c->head_dim)
-                            : attention_sized<DT, false, kWaves>(c->head_dim);
+    return lone             ? attention_sized<DT, true, kLoneWaves, VIEW>(c->head_dim)
+           : whole_tiles(c) ? attention_sized<DT, true, kWaves, VIEW>(c->head_dim)
+                            : attention_sized<DT, false, kWaves, VIEW>(c->head_dim);
 }
 
 }  // namespace gattn

@@ -131,30 +131,6 @@ int whole_sinks(int sinks, int tile, int limit)
     return (int)(n < most ? n : most);
 }
 
-template <int DT, bool WHOLE, int WAVES>
-const void* view_sized(int dim)
-{
-    if constexpr (WHOLE) {
-        if (dim == 64)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 64, true, true, WAVES, true>);
-        if (dim == 128)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 128, true, true, WAVES, true>);
-        if (dim == 256)
-            return reinterpret_cast<const void*>(&attention_kernel<DT, 256, true, true, WAVES, true>);
-    }
-    return dim <= 64    ? reinterpret_cast<const void*>(&attention_kernel<DT, 64, WHOLE, false, WAVES, true>)
-           : dim <= 128 ? reinterpret_cast<const void*>(&attention_kernel<DT, 128, WHOLE, false, WAVES, true>)
-                        : reinterpret_cast<const void*>(&attention_kernel<DT, 256, WHOLE, false, WAVES, true>);
-}
-
-template <int DT>
-const void* view_for(const gemv_kv_cache* c, bool lone)
-{
-    return lone             ? view_sized<DT, true, kLoneWaves>(c->head_dim)
-           : whole_tiles(c) ? view_sized<DT, true, kWaves>(c->head_dim)
-                            : view_sized<DT, false, kWaves>(c->head_dim);
-}
-
 enum Form { kPrompt, kPrefix };
 
 template <int DT, int DP, int RUN, bool EXACT>
@@ -441,7 +417,8 @@ int gemv_prompt_attention(const gemv_kv_cache* cache, const gemv_kv_batch* batch
         if (!fits(grid, block))
             return GEMV_E_UNSUPPORTED;
         void* args[] = {(void*)&a};
-        const void* fn = cache->dtype == GEMV_F16 ? view_for<kF16>(cache, p.split.lone) : view_for<kBF16>(cache, p.split.lone);
+        const void* fn = cache->dtype == GEMV_F16 ? attention_for<kF16, true>(cache, p.split.lone)
+                                                  : attention_for<kBF16, true>(cache, p.split.lone);
         if (int rc = launch(fn, grid, block, args, stream); rc != GEMV_OK || !p.joined)
             return rc;
         j.from[0] = Source{a.part_ms, a.part_out, a.parts, nullptr, 0};
