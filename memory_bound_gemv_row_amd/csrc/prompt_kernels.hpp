@@ -116,7 +116,8 @@ __device__ __forceinline__ float add_pair([[maybe_unused]] unsigned pair, float 
 // LDS wait for such loads, those into the other buffer too; the kernel waits for
 // them itself, before the barrier that hands a buffer over.  s_nop: five steps
 // between a vector instruction that writes a scalar register and its use as a
-// descriptor, and one after m0 is set.
+// descriptor, and one after m0 is set.  (m0 cannot be named as changed: it is reserved,
+// and the compiler sets it right before each use of its own.)
 __device__ __forceinline__ void piece_to_lds([[maybe_unused]] u32x4 from, [[maybe_unused]] unsigned offset,
                                              [[maybe_unused]] unsigned to)
 {
@@ -322,14 +323,19 @@ __device__ const u32x4 kZeros[1] = {{0, 0, 0, 0}};
 // pages of 5; 2 x 8192, 32/8 heads of 128: 610, 633, 736).
 //
 // Bound, where prompts are long, by the matrix and the vector units in turn: both
-// are busy 45 % of the time and a SIMD's two waves only partly overlap, for all
-// wait for each tile of keys at one barrier (2 x 16384 tokens through a window of
-// 4096, 32/8 heads of 128: 1706 to 1780 us, 919 to 959 TFLOP/s; the products and
+// are busy 45 % of the time, for a wave takes its products, maximum, powers and
+// products one after another, and that a SIMD's other wave does something else meanwhile is
+// left to chance.  (Up to 128 that one is of another workgroup, with a barrier of its
+// own; over 128 both wait at one.)  2 x 16384 tokens through a window of
+// 4096, 32/8 heads of 128: 1710 to 1850 us by card, 886 to 957 TFLOP/s; the products and
 // barriers alone take 64 % of a long prompt's time, exponentials 10 %, reads of
-// LDS 16 %, loads 17 %, the maximum 3 %, each taken out by itself).  Where rows
-// are few, by memory: 4 x 7 tokens behind up to 65536 read 715 MB in 131 us.  Of
-// a few hundred rows, by the 1.1 to 2 us that a step takes however few waves
-// there are.
+// LDS 16 %, loads 17 %, the maximum 3 %, each taken out by itself.  Heads of 64 have half
+// the products for as many powers, whose 26 cycles for 64 of them are more than
+// the products' 16: 4 x 8192 tokens of 16 heads 260 us of vector instructions alone.
+// Where rows are few, by memory: 4 x 7 tokens behind up to 65536 read 715 MB in 131 us.
+// Of a few hundred rows, by the 1.1 to 2 us that a step takes however few waves
+// there are.  Heads of over 128 keep 22 to 132 registers in scratch memory, most of
+// them read outside of the loop over whole tiles, and take their logits twice.
 //
 // Places in LDS: piece c (16 bytes) of key row r lies at c ^ swizzle(r), such
 // that the 16 rows that a read of keys takes at a time, and the four rows of
